@@ -30,6 +30,13 @@ MOE_ERR_LAUNCH = 4
 MOE_ROUTE_NORMALIZE = 1
 MOE_COMBINE_OUT_FP32 = 1
 MOE_FLOOR_NT_STORE = 1
+MOE_SCORE_SIGMOID = 2
+MOE_GROUP_TOP2 = 4
+MOE_LOGITS_BF16 = 8
+MOE_PRODUCT_GATED = 1
+MOE_GRAD_FP32 = 1
+MOE_GRAD_ACCUMULATE = 2
+MOE_ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 EXPORTS = ("moe_route_topk", "moe_route_topk_grouped", "moe_layout_workspace_size", "moe_dispatch_layout",
            "moe_route_dispatch_layout_workspace_size", "moe_route_dispatch_layout", "moe_dispatch_layout_noalloc",
@@ -37,7 +44,9 @@ EXPORTS = ("moe_route_topk", "moe_route_topk_grouped", "moe_layout_workspace_siz
            "moe_dispatch_permute_fp8", "moe_fp8_dequant", "moe_recv_regroup_workspace_size",
            "moe_recv_regroup_layout", "moe_recv_regroup", "moe_recv_ungroup",
            "moe_expert_linear_workspace_size", "moe_expert_linear", "moe_expert_linear_return",
-           "moe_expert_return_slots", "moe_hbm_floor", "moe_status_string")
+           "moe_expert_return_slots", "moe_hbm_floor", "moe_route_scored", "moe_route_scored_backward",
+           "moe_combine_backward", "moe_expert_product", "moe_expert_product_dgrad",
+           "moe_expert_product_wgrad_workspace_size", "moe_expert_product_wgrad", "moe_status_string")
 
 
 class MoeError(RuntimeError):
@@ -77,6 +86,14 @@ def _load_library() -> ctypes.CDLL:
                                              ctypes.c_size_t, P]
     lib.moe_expert_return_slots.argtypes = [ctypes.POINTER(ctypes.c_int32)]
     lib.moe_hbm_floor.argtypes = [P, i64, P, i64, u32, P]
+    f32 = ctypes.c_float
+    lib.moe_route_scored.argtypes = [P, P, i64, i32, i32, i32, i32, f32, u32, P, P, P]
+    lib.moe_route_scored_backward.argtypes = [P, P, P, i64, i32, i32, f32, u32, P, P]
+    lib.moe_combine_backward.argtypes = [P, P, i64, P, P, i64, i32, i32, u32, P, P, P]
+    lib.moe_expert_product.argtypes = [P, P, i32, i64, i32, i32, P, P, P, i32, u32, P, P, P]
+    lib.moe_expert_product_dgrad.argtypes = [P, P, i32, i64, i32, i32, P, P, i32, u32, P, P]
+    lib.moe_expert_product_wgrad_workspace_size.argtypes = [i32, i64, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
+    lib.moe_expert_product_wgrad.argtypes = [P, P, P, i32, i64, i32, i32, u32, P, P, P, ctypes.c_size_t, P]
     lib.moe_status_string.argtypes = [ctypes.c_int]
     lib.moe_status_string.restype = ctypes.c_char_p
     for name in EXPORTS[:-1]:
@@ -465,3 +482,205 @@ def moe_hbm_floor(src: torch.Tensor, read_bytes: int, dst: torch.Tensor, write_b
     _check("moe_hbm_floor", lib.moe_hbm_floor(
         src.data_ptr() or None, read_bytes, dst.data_ptr() or None, write_bytes,
         MOE_FLOOR_NT_STORE if nt_store else 0, _stream(stream)))
+
+
+def _shaped(t: Optional[torch.Tensor], name: str, shape, dtypes, device):
+    """The pointer of t, which must be a contiguous `shape` tensor on `device` (None passes)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    p = _ptr(t, dtypes, name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, other arguments on {device}")
+    return p
+
+
+def _need(t, name: str, ndim: int):
+    """t itself, which must be a GPU tensor of ndim dimensions."""
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t
+
+
+def _on(device):
+    """Makes `device` current for the launch: kernels run on their tensors' GPU."""
+    return torch.cuda.device(device)
+
+
+def _score_flags(logits: torch.Tensor, scores: str, normalize: bool) -> int:
+    if scores not in ("softmax", "sigmoid"):
+        raise ValueError(f"scores must be 'softmax' or 'sigmoid', got {scores!r}")
+    return ((MOE_SCORE_SIGMOID if scores == "sigmoid" else 0) | (MOE_ROUTE_NORMALIZE if normalize else 0)
+            | (MOE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else 0))
+
+
+_LOGITS = (torch.float32, torch.bfloat16)
+
+
+def moe_route_scored(logits: torch.Tensor, bias: Optional[torch.Tensor], k: int, n_groups: int = 1,
+                     topk_groups: int = 1, scores: str = "softmax", normalize: bool = True,
+                     group_top2: bool = False, scale: float = 1.0, topk_idx: Optional[torch.Tensor] = None,
+                     topk_w: Optional[torch.Tensor] = None, stream=None):
+    """Top-k experts by softmax or sigmoid score plus selection bias, and their
+    weights (see moe_route_scored). logits are float32 or bf16."""
+    T, E = _need(logits, "logits", 2).shape
+    dev = logits.device
+    flags = _score_flags(logits, scores, normalize) | (MOE_GROUP_TOP2 if group_top2 else 0)
+    if topk_idx is None:
+        topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if topk_w is None:
+        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    with _on(dev):
+        _check("moe_route_scored", lib.moe_route_scored(
+            _ptr(logits, _LOGITS, "logits", 2), _shaped(bias, "bias", (E,), _F32, dev), T, E, k, n_groups,
+            topk_groups, scale, flags, _shaped(topk_idx, "topk_idx", (T, k), _I32, dev),
+            _shaped(topk_w, "topk_w", (T, k), _F32, dev), _stream(stream)))
+    return topk_idx, topk_w
+
+
+def moe_route_scored_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_w: torch.Tensor,
+                              scores: str = "softmax", normalize: bool = True, scale: float = 1.0,
+                              grad_logits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dL/dlogits from dL/dtopk_w (see moe_route_scored_backward), in the
+    logits' type."""
+    T, E = _need(logits, "logits", 2).shape
+    dev = logits.device
+    k = _need(topk_idx, "topk_idx", 2).shape[1]
+    if grad_logits is None:
+        grad_logits = torch.empty_like(logits, memory_format=torch.contiguous_format)
+    with _on(dev):
+        _check("moe_route_scored_backward", lib.moe_route_scored_backward(
+            _ptr(logits, _LOGITS, "logits", 2), _shaped(topk_idx, "topk_idx", (T, k), _I32, dev),
+            _shaped(grad_w, "grad_w", (T, k), _F32, dev), T, E, k, scale, _score_flags(logits, scores, normalize),
+            _shaped(grad_logits, "grad_logits", (T, E), (logits.dtype,), dev), _stream(stream)))
+    return grad_logits
+
+
+def moe_combine_backward(grad_out: torch.Tensor, y: Optional[torch.Tensor], pos: torch.Tensor,
+                         topk_w: Optional[torch.Tensor], grad_y: Optional[torch.Tensor] = None,
+                         grad_w: Optional[torch.Tensor] = None, need_y: bool = True, need_w: bool = True,
+                         y_rows: Optional[int] = None, stream=None):
+    """(grad_y, grad_w): gradients of moe_combine_reduce's expert rows and gate
+    weights (see moe_combine_backward). need_y or need_w False leaves that one
+    out (None), and topk_w or y with it; rows of a grad_y allocated here that
+    no replica points at are not initialised. y_rows is needed without y and
+    grad_y."""
+    T, H = _need(grad_out, "grad_out", 2).shape
+    dev = grad_out.device
+    k = _need(pos, "pos", 2).shape[1]
+    if y_rows is None:
+        rows = y if y is not None else grad_y
+        if rows is None:
+            raise ValueError("y_rows is needed without y and grad_y")
+        y_rows = rows.shape[0]
+    if need_w and y is None:
+        raise ValueError("grad_w needs y")
+    if need_y and topk_w is None:
+        raise ValueError("grad_y needs topk_w")
+    if need_y and grad_y is None:
+        grad_y = torch.empty((y_rows, H), dtype=torch.bfloat16, device=dev)
+    if need_w and grad_w is None:
+        grad_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    grad_y, grad_w = grad_y if need_y else None, grad_w if need_w else None
+    fp32 = grad_out.dtype == torch.float32
+    with _on(dev):
+        _check("moe_combine_backward", lib.moe_combine_backward(
+            _ptr(grad_out, _F32 if fp32 else _BF16, "grad_out", 2), _shaped(y, "y", (y_rows, H), _BF16, dev), y_rows,
+            _shaped(pos, "pos", (T, k), _I32, dev), _shaped(topk_w, "topk_w", (T, k), _F32, dev), T, H, k,
+            MOE_COMBINE_OUT_FP32 if fp32 else 0, _shaped(grad_y, "grad_y", (y_rows, H), _BF16, dev),
+            _shaped(grad_w, "grad_w", (T, k), _F32, dev), _stream(stream)))
+    return grad_y, grad_w
+
+
+def _act(act: str) -> int:
+    if act not in MOE_ACT:
+        raise ValueError(f"act must be one of {sorted(MOE_ACT)}, got {act!r}")
+    return MOE_ACT[act]
+
+
+def moe_expert_product(x: torch.Tensor, expert_offsets: torch.Tensor, W: torch.Tensor,
+                       bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                       act: str = "none", gated: bool = False, y: Optional[torch.Tensor] = None,
+                       pre: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y [max_rows, O]: each expert-major row times its expert's W[l]^T, with
+    bias, activation (none, relu, silu, gelu, gelu_tanh), gate and residual
+    (see moe_expert_product). W is [E_l, O, H], or [E_l, 2 O, H] gated; pre
+    ([max_rows, O or 2 O]), when given, receives the pre-activations. Rows past
+    the last expert's are not written."""
+    max_rows, H = _need(x, "x", 2).shape
+    dev = x.device
+    El, wide, _ = _need(W, "W", 3).shape
+    if gated and wide % 2:
+        raise ValueError("a gated W holds gate and up outputs in equal number")
+    O = wide // 2 if gated else wide
+    if y is None:
+        y = torch.empty((max_rows, O), dtype=torch.bfloat16, device=dev)
+    with _on(dev):
+        _check("moe_expert_product", lib.moe_expert_product(
+            _ptr(x, _BF16, "x", 2), _shaped(expert_offsets, "expert_offsets", (El + 1,), _I32, dev), El, max_rows, H,
+            O, _shaped(W, "W", (El, wide, H), _BF16, dev), _shaped(bias, "bias", (El, wide), _BF16, dev),
+            _shaped(residual, "residual", (max_rows, O), _BF16, dev), _act(act), MOE_PRODUCT_GATED if gated else 0,
+            _shaped(pre, "pre", (max_rows, wide), _BF16, dev), _shaped(y, "y", (max_rows, O), _BF16, dev),
+            _stream(stream)))
+    return y
+
+
+def moe_expert_product_dgrad(grad_y: torch.Tensor, expert_offsets: torch.Tensor, W: torch.Tensor,
+                             pre: Optional[torch.Tensor] = None, act: str = "none", gated: bool = False,
+                             grad_x: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """grad_y times W, through the activation (of pre) that made the product's
+    input (see moe_expert_product_dgrad): [max_rows, H], or [max_rows, 2 H]
+    gated."""
+    max_rows, O = _need(grad_y, "grad_y", 2).shape
+    dev = grad_y.device
+    El, _, H = _need(W, "W", 3).shape
+    wide = 2 * H if gated else H
+    if grad_x is None:
+        grad_x = torch.empty((max_rows, wide), dtype=torch.bfloat16, device=dev)
+    with _on(dev):
+        _check("moe_expert_product_dgrad", lib.moe_expert_product_dgrad(
+            _ptr(grad_y, _BF16, "grad_y", 2), _shaped(expert_offsets, "expert_offsets", (El + 1,), _I32, dev), El,
+            max_rows, O, H, _shaped(W, "W", (El, O, H), _BF16, dev), _shaped(pre, "pre", (max_rows, wide), _BF16, dev),
+            _act(act), MOE_PRODUCT_GATED if gated else 0, _shaped(grad_x, "grad_x", (max_rows, wide), _BF16, dev),
+            _stream(stream)))
+    return grad_x
+
+
+def moe_expert_product_wgrad_workspace_size(E_l: int, max_rows: int, O: int, H: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_expert_product_wgrad_workspace_size",
+           lib.moe_expert_product_wgrad_workspace_size(E_l, max_rows, O, H, ctypes.byref(n)))
+    return n.value
+
+
+def moe_expert_product_wgrad(grad_y: torch.Tensor, x: torch.Tensor, expert_offsets: torch.Tensor,
+                             grad_W: Optional[torch.Tensor] = None, grad_bias: Optional[torch.Tensor] = None,
+                             accumulate: bool = False, workspace: Optional[torch.Tensor] = None,
+                             stream=None) -> torch.Tensor:
+    """grad_W [E_l, O, H] (bf16 when allocated here; float32 when given so) and,
+    when given, grad_bias [E_l, O] float32 (see moe_expert_product_wgrad).
+    accumulate adds to both, which must then be given, grad_W in float32."""
+    max_rows, O = _need(grad_y, "grad_y", 2).shape
+    dev = grad_y.device
+    H = _need(x, "x", 2).shape[1]
+    El = _need(expert_offsets, "expert_offsets", 1).shape[0] - 1
+    if grad_W is None:
+        if accumulate:
+            raise ValueError("accumulate needs grad_W")
+        grad_W = torch.empty((El, O, H), dtype=torch.bfloat16, device=dev)
+    fp32 = grad_W.dtype == torch.float32
+    need = moe_expert_product_wgrad_workspace_size(El, max_rows, O, H)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    with _on(dev):
+        _check("moe_expert_product_wgrad", lib.moe_expert_product_wgrad(
+            _ptr(grad_y, _BF16, "grad_y", 2), _shaped(x, "x", (max_rows, H), _BF16, dev),
+            _shaped(expert_offsets, "expert_offsets", (El + 1,), _I32, dev), El, max_rows, O, H,
+            (MOE_GRAD_FP32 if fp32 else 0) | (MOE_GRAD_ACCUMULATE if accumulate else 0),
+            _shaped(grad_W, "grad_W", (El, O, H), _F32 if fp32 else _BF16, dev),
+            _shaped(grad_bias, "grad_bias", (El, O), _F32, dev), _ptr(workspace, (torch.uint8,), "workspace"),
+            0 if workspace is None else workspace.numel(), _stream(stream)))
+    return grad_W

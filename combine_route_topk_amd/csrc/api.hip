@@ -104,6 +104,39 @@ moe_status_t regroup_rows(const uint16_t *src, const int32_t *map, const int32_t
                                              static_cast<hipStream_t>(stream)));
 }
 
+// The scored router's sizes and flags (`allowed`), and its groups.
+moe_status_t check_scored(int64_t T, int32_t E, int32_t k, float scale, uint32_t flags,
+                          uint32_t allowed)
+{
+    moe_status_t s = check_tokens(T, k);
+    if (s != MOE_OK)
+        return s;
+    if ((s = check_experts(E, k)) != MOE_OK)
+        return s;
+    if ((flags & ~allowed) || !(scale - scale == 0.f))  // NaN and infinities fail the second
+        return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+moe::ScoreOpts score_opts(float scale, uint32_t flags)
+{
+    return {(flags & MOE_SCORE_SIGMOID) != 0, (flags & MOE_ROUTE_NORMALIZE) != 0,
+            (flags & MOE_GROUP_TOP2) != 0, (flags & MOE_LOGITS_BF16) != 0, scale};
+}
+
+// The experts' products: sizes and the row bound.
+moe_status_t check_product(int32_t El, int64_t max_rows, int32_t H, int32_t O)
+{
+    if (El < 1 || max_rows < 0)
+        return MOE_ERR_INVALID_ARG;
+    if (El > moe::kMaxLocalExperts || max_rows >= kMaxAssignments)
+        return MOE_ERR_UNSUPPORTED;
+    moe_status_t s = check_hidden(H);
+    return s != MOE_OK ? s : check_hidden(O);
+}
+
+bool known_act(int32_t act) { return act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH; }
+
 }  // namespace
 
 extern "C" {
@@ -505,6 +538,176 @@ moe_status_t moe_expert_return_slots(int32_t *slots)
         return MOE_ERR_LAUNCH;
     *slots = n;
     return MOE_OK;
+}
+
+moe_status_t moe_route_scored(const void *logits, const float *bias, int64_t T, int32_t E,
+                              int32_t k, int32_t n_groups, int32_t topk_groups, float scale,
+                              uint32_t flags, int32_t *topk_idx, float *topk_w, void *stream)
+{
+    moe_status_t s = check_scored(T, E, k, scale, flags,
+                                  MOE_ROUTE_NORMALIZE | MOE_SCORE_SIGMOID | MOE_GROUP_TOP2 |
+                                      MOE_LOGITS_BF16);
+    if (s != MOE_OK)
+        return s;
+    if (n_groups < 1 || E % n_groups != 0 || topk_groups < 1 || topk_groups > n_groups ||
+        (int64_t)k > (int64_t)topk_groups * (E / n_groups))
+        return MOE_ERR_INVALID_ARG;
+    if (n_groups > kMaxGroups)
+        return MOE_ERR_UNSUPPORTED;
+    if (T == 0)
+        return MOE_OK;
+    if (!logits || !topk_idx || !topk_w)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(logits, flags & MOE_LOGITS_BF16 ? 2 : 4) || !aligned(bias, 4) ||
+        !aligned(topk_idx, 4) || !aligned(topk_w, 4))
+        return MOE_ERR_INVALID_ARG;
+    const int32_t groups = topk_groups == n_groups ? 0 : n_groups;  // all groups: no limit
+    return from_hip(moe::launch_route_scored(logits, bias, T, E, k, groups, topk_groups,
+                                             score_opts(scale, flags), topk_idx, topk_w,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_route_scored_backward(const void *logits, const int32_t *topk_idx,
+                                       const float *grad_w, int64_t T, int32_t E, int32_t k,
+                                       float scale, uint32_t flags, void *grad_logits,
+                                       void *stream)
+{
+    moe_status_t s = check_scored(T, E, k, scale, flags,
+                                  MOE_ROUTE_NORMALIZE | MOE_SCORE_SIGMOID | MOE_LOGITS_BF16);
+    if (s != MOE_OK)
+        return s;
+    if (T == 0)
+        return MOE_OK;
+    if (!logits || !topk_idx || !grad_w || !grad_logits)
+        return MOE_ERR_INVALID_ARG;
+    const uintptr_t size = flags & MOE_LOGITS_BF16 ? 2 : 4;
+    if (!aligned(logits, size) || !aligned(grad_logits, size) || !aligned(topk_idx, 4) ||
+        !aligned(grad_w, 4))
+        return MOE_ERR_INVALID_ARG;
+    return from_hip(moe::launch_route_scored_backward(logits, topk_idx, grad_w, T, E, k,
+                                                      score_opts(scale, flags), grad_logits,
+                                                      static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_combine_backward(const void *grad_out, const uint16_t *y, int64_t y_rows,
+                                  const int32_t *pos, const float *topk_w, int64_t T, int32_t H,
+                                  int32_t k, uint32_t flags, uint16_t *grad_y, float *grad_w,
+                                  void *stream)
+{
+    moe_status_t s = check_tokens(T, k);
+    if (s != MOE_OK)
+        return s;
+    if ((s = check_hidden(H)) != MOE_OK)
+        return s;
+    if ((flags & ~MOE_COMBINE_OUT_FP32) || y_rows < 0)
+        return MOE_ERR_INVALID_ARG;
+    if (y_rows >= kMaxAssignments)
+        return MOE_ERR_UNSUPPORTED;
+    if (T == 0)
+        return MOE_OK;
+    if (y_rows == 0) {  // every replica is dropped: only grad_w is written
+        if (!grad_w && !grad_y)
+            return MOE_ERR_INVALID_ARG;
+    } else if ((!grad_y && !grad_w) || (grad_w && !y) || (grad_y && !topk_w)) {
+        return MOE_ERR_INVALID_ARG;
+    }
+    if (!grad_out || !pos)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(grad_out, 16) || !aligned(y, 16) || !aligned(grad_y, 16) || !aligned(pos, 4) ||
+        !aligned(topk_w, 4) || !aligned(grad_w, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (y_rows == 0) {
+        grad_y = nullptr;
+        if (!grad_w)
+            return MOE_OK;
+    }
+    return from_hip(moe::launch_combine_backward(grad_out, (flags & MOE_COMBINE_OUT_FP32) != 0, y,
+                                                 y_rows, pos, topk_w, T, H, k, grad_y, grad_w,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_expert_product(const uint16_t *x, const int32_t *expert_offsets, int32_t E_l,
+                                int64_t max_rows, int32_t H, int32_t O, const uint16_t *W,
+                                const uint16_t *bias, const uint16_t *residual, int32_t act,
+                                uint32_t flags, uint16_t *pre, uint16_t *y, void *stream)
+{
+    moe_status_t s = check_product(E_l, max_rows, H, O);
+    if (s != MOE_OK)
+        return s;
+    if ((flags & ~MOE_PRODUCT_GATED) || !known_act(act))
+        return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0)
+        return MOE_OK;
+    if (!x || !expert_offsets || !W || !y)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(W, 16) || !aligned(y, 16) || !aligned(bias, 16) ||
+        !aligned(residual, 16) || !aligned(pre, 16) || !aligned(expert_offsets, 4))
+        return MOE_ERR_INVALID_ARG;
+    return from_hip(moe::launch_expert_product(x, expert_offsets, E_l, max_rows, H, O, W, bias,
+                                               residual, act, (flags & MOE_PRODUCT_GATED) != 0,
+                                               pre, y, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_expert_product_dgrad(const uint16_t *grad_y, const int32_t *expert_offsets,
+                                      int32_t E_l, int64_t max_rows, int32_t O, int32_t H,
+                                      const uint16_t *W, const uint16_t *pre, int32_t act,
+                                      uint32_t flags, uint16_t *grad_x, void *stream)
+{
+    moe_status_t s = check_product(E_l, max_rows, H, O);
+    if (s != MOE_OK)
+        return s;
+    if ((flags & ~MOE_PRODUCT_GATED) || !known_act(act))
+        return MOE_ERR_INVALID_ARG;
+    if (!pre && (flags || act != MOE_ACT_NONE) && max_rows > 0)
+        return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0)
+        return MOE_OK;
+    if (!grad_y || !expert_offsets || !W || !grad_x)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(grad_y, 16) || !aligned(W, 16) || !aligned(pre, 16) || !aligned(grad_x, 16) ||
+        !aligned(expert_offsets, 4))
+        return MOE_ERR_INVALID_ARG;
+    return from_hip(moe::launch_expert_dgrad(grad_y, expert_offsets, E_l, max_rows, O, H, W, pre,
+                                             act, (flags & MOE_PRODUCT_GATED) != 0, grad_x,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_expert_product_wgrad_workspace_size(int32_t E_l, int64_t max_rows, int32_t O,
+                                                     int32_t H, size_t *bytes)
+{
+    if (!bytes)
+        return MOE_ERR_INVALID_ARG;
+    moe_status_t s = check_product(E_l, max_rows, H, O);
+    if (s != MOE_OK)
+        return s;
+    *bytes = moe::wgrad_workspace_bytes(E_l, max_rows, O, H);
+    return MOE_OK;
+}
+
+moe_status_t moe_expert_product_wgrad(const uint16_t *grad_y, const uint16_t *x,
+                                      const int32_t *expert_offsets, int32_t E_l,
+                                      int64_t max_rows, int32_t O, int32_t H, uint32_t flags,
+                                      void *grad_W, float *grad_bias, void *workspace,
+                                      size_t workspace_bytes, void *stream)
+{
+    moe_status_t s = check_product(E_l, max_rows, H, O);
+    if (s != MOE_OK)
+        return s;
+    if ((flags & ~(MOE_GRAD_FP32 | MOE_GRAD_ACCUMULATE)) ||
+        ((flags & MOE_GRAD_ACCUMULATE) && !(flags & MOE_GRAD_FP32)))
+        return MOE_ERR_INVALID_ARG;
+    if ((max_rows > 0 && (!grad_y || !x)) || !expert_offsets || !grad_W)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(grad_y, 16) || !aligned(x, 16) || !aligned(grad_W, 16) ||
+        !aligned(grad_bias, 4) || !aligned(expert_offsets, 4))
+        return MOE_ERR_INVALID_ARG;
+    const size_t need = moe::wgrad_workspace_bytes(E_l, max_rows, O, H);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+        return MOE_ERR_WORKSPACE;
+    return from_hip(moe::launch_expert_wgrad(
+        grad_y, x, expert_offsets, E_l, max_rows, O, H, (flags & MOE_GRAD_FP32) != 0,
+        (flags & MOE_GRAD_ACCUMULATE) != 0, grad_W, grad_bias, workspace,
+        static_cast<hipStream_t>(stream)));
 }
 
 moe_status_t moe_hbm_floor(const void *src, int64_t read_bytes, void *dst, int64_t write_bytes,

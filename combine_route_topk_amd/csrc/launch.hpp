@@ -108,6 +108,43 @@ hipError_t launch_regroup_rows(const uint16_t *src, const int32_t *map, const in
                                int64_t max_rows, int32_t H, bool gather, uint16_t *dst,
                                hipStream_t stream);
 
+// Scored routing and its gradient (score_route.hip). n_groups == 0: no groups.
+struct ScoreOpts {
+    bool sigmoid, normalize, top2, bf16;
+    float scale;
+};
+hipError_t launch_route_scored(const void *logits, const float *bias, int64_t T, int32_t E,
+                               int32_t k, int32_t n_groups, int32_t topk_groups,
+                               const ScoreOpts &o, int32_t *topk_idx, float *topk_w,
+                               hipStream_t stream);
+hipError_t launch_route_scored_backward(const void *logits, const int32_t *topk_idx,
+                                        const float *grad_w, int64_t T, int32_t E, int32_t k,
+                                        const ScoreOpts &o, void *grad_logits,
+                                        hipStream_t stream);
+
+// The combine's gradient (combine_backward.hip); grad_y or grad_w may be NULL.
+hipError_t launch_combine_backward(const void *grad_out, bool fp32, const uint16_t *y,
+                                   int64_t y_rows, const int32_t *pos, const float *topk_w,
+                                   int64_t T, int32_t H, int32_t k, uint16_t *grad_y,
+                                   float *grad_w, hipStream_t stream);
+
+// The experts' products (product.hip) and their weight gradient
+// (product_wgrad.hip). act is a moe_act value.
+constexpr int32_t kMaxLocalExperts = 1024;
+hipError_t launch_expert_product(const uint16_t *x, const int32_t *off, int32_t El,
+                                 int64_t max_rows, int32_t H, int32_t O, const uint16_t *W,
+                                 const uint16_t *bias, const uint16_t *residual, int32_t act,
+                                 bool gated, uint16_t *pre, uint16_t *y, hipStream_t stream);
+hipError_t launch_expert_dgrad(const uint16_t *grad_y, const int32_t *off, int32_t El,
+                               int64_t max_rows, int32_t O, int32_t H, const uint16_t *W,
+                               const uint16_t *pre, int32_t act, bool gated, uint16_t *grad_x,
+                               hipStream_t stream);
+size_t wgrad_workspace_bytes(int32_t El, int64_t max_rows, int32_t O, int32_t H);
+hipError_t launch_expert_wgrad(const uint16_t *grad_y, const uint16_t *x, const int32_t *off,
+                               int32_t El, int64_t max_rows, int32_t O, int32_t H, bool fp32,
+                               bool accumulate, void *grad_W, float *grad_bias, void *workspace,
+                               hipStream_t stream);
+
 // Synthetic floor: a contiguous streaming read and write (floor.hip).
 hipError_t launch_hbm_floor(const void *src, int64_t read_bytes, void *dst, int64_t write_bytes,
                             bool nt_store, hipStream_t stream);

@@ -1,0 +1,140 @@
+// product_device.hpp -- what the experts' products and their gradients share:
+// the row tiles of an expert-major buffer, and the activations.
+#pragma once
+
+#include "device.hpp"
+#include "launch.hpp"
+
+namespace moe {
+namespace {
+
+// Expert l's rows, kept inside [0, max_rows] whatever the offsets hold.
+struct Rows {
+    int32_t begin, end;
+};
+__device__ __forceinline__ Rows expert_rows(const int32_t *__restrict__ off, int32_t l, int32_t max_rows)
+{
+    Rows r;
+    r.begin = min(max(off[l], 0), max_rows);
+    r.end = min(max(off[l + 1], r.begin), max_rows);
+    return r;
+}
+
+// first[l] = row tiles of BM rows before expert l, for l <= El (El <= 1024);
+// returns their total. Every thread of the block takes part; `first` is in
+// LDS and ready after the call. One pass over at most 1025 offsets by the
+// block itself costs a launch less than a table written by another kernel.
+template <int THREADS, int BM>
+__device__ int32_t plan_row_tiles(const int32_t *__restrict__ off, int32_t El, int32_t max_rows,
+                                  int32_t *first)
+{
+    constexpr int PER = (kMaxLocalExperts + THREADS - 1) / THREADS;
+    constexpr int WAVES = THREADS / kWave;
+    __shared__ int32_t wave_total[WAVES];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave;
+    int32_t n[PER], part = 0;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        const int l = tid * PER + u;
+        n[u] = 0;
+        if (l < El) {
+            const Rows r = expert_rows(off, l, max_rows);
+            n[u] = (int32_t)(((int64_t)r.end - r.begin + BM - 1) / BM);
+        }
+        part += n[u];
+    }
+    const int32_t inc = wave_inclusive_sum(part);
+    if (lane == kWave - 1)
+        wave_total[w] = inc;
+    __syncthreads();
+    int32_t run = inc - part, all = 0;
+#pragma unroll
+    for (int u = 0; u < WAVES; ++u) {
+        run += u < w ? wave_total[u] : 0;
+        all += wave_total[u];
+    }
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        const int l = tid * PER + u;
+        if (l < El)
+            first[l] = run;
+        run += n[u];
+    }
+    if (tid == 0)
+        first[El] = all;
+    __syncthreads();
+    return all;
+}
+
+// the expert whose tiles hold tile t: the largest l with first[l] <= t
+__device__ __forceinline__ int32_t tile_expert(const int32_t *first, int32_t El, int32_t t)
+{
+    int32_t lo = 0, hi = El - 1;
+    while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// act(z) and act'(z) in float32, ACT a moe_act value. Arguments of the
+// exponentials are bounded where a product with an overflowed factor would
+// give NaN: beyond |z| = 30 both GELUs' cdf and derivative are 0 or 1 in
+// float32, and SiLU's are once |z| > 104.
+enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+
+__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kSqrt2OverPi = 0.79788456080286536f;
+constexpr float kGeluCubic = 0.044715f;
+
+// with u = sqrt(2 / pi) (z + c z^3), (1 + tanh u) / 2 = sigmoid(2 u)
+__device__ __forceinline__ float gelu_tanh_cdf(float z)
+{
+    const float b = fminf(fmaxf(z, -30.f), 30.f);
+    return sigmoid(2.f * kSqrt2OverPi * (b + kGeluCubic * b * b * b));
+}
+
+template <int ACT>
+__device__ __forceinline__ float act(float z)
+{
+    switch (ACT) {
+    case kActRelu: return z > 0.f ? z : (z != z ? z : 0.f);
+    case kActSilu: return z * sigmoid(z);
+    case kActGelu: return 0.5f * z * erfcf(-z * kSqrtHalf);
+    case kActGeluTanh: return z * gelu_tanh_cdf(z);
+    default: return z;
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_grad(float z)
+{
+    switch (ACT) {
+    case kActRelu: return z > 0.f ? 1.f : (z != z ? z : 0.f);
+    case kActSilu: {
+        const float b = fminf(fmaxf(z, -104.f), 104.f), p = sigmoid(b);
+        return p * (1.f + b * (1.f - p));
+    }
+    case kActGelu: {
+        const float b = fminf(fmaxf(z, -30.f), 30.f);
+        return 0.5f * erfcf(-b * kSqrtHalf) + b * expf(-0.5f * b * b) * kInvSqrt2Pi;
+    }
+    case kActGeluTanh: {
+        const float b = fminf(fmaxf(z, -30.f), 30.f), p = gelu_tanh_cdf(b);
+        return p + 2.f * b * p * (1.f - p) * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * b * b);
+    }
+    default: return 1.f;
+    }
+}
+
+__device__ __forceinline__ float bf16_to_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ uint16_t f32_to_bf16(float v) { return (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu); }
+
+}  // namespace
+}  // namespace moe

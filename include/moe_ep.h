@@ -528,6 +528,227 @@ moe_status_t moe_expert_linear_return(const uint16_t *recv, const int32_t *recv_
  * (resident blocks per compute unit x compute units). */
 moe_status_t moe_expert_return_slots(int32_t *slots);
 
+/*
+ * Scored routing, the combine's gradient and the experts' products, forward
+ * and backward: the rest of a trained mixture-of-experts layer around the
+ * dispatch path. A layer's forward pass is route -> layout -> permute ->
+ * expert products -> combine; its backward pass is moe_combine_backward ->
+ * the products' gradients -> moe_combine_reduce with every weight 1 (the
+ * permute's gradient: the sum of a token's replica rows) ->
+ * moe_route_scored_backward.
+ */
+
+/* moe_route_scored flags, beside MOE_ROUTE_NORMALIZE */
+#define MOE_SCORE_SIGMOID 2u  /* scores are sigmoid(logit); else softmax over all E */
+#define MOE_GROUP_TOP2 4u     /* a group's score is the sum of its two best, not its best */
+#define MOE_LOGITS_BF16 8u    /* logits (and their gradient) are bf16, else float32 */
+
+/*
+ * moe_route_scored -- top-k routing on scores: the selection bias is added
+ * to the score (moe_route_topk adds it to the logit), scores are a sigmoid
+ * of each logit or the softmax of all, and groups may be ranked by their
+ * two best.
+ *
+ * Defined by: ai-from-scratch "19. All-to-all", "Why the router can ruin
+ * your day" (the balancing bias takes part in the selection only) and
+ * "DeepSeek's numbers" (each token limited to a few groups of experts).
+ *
+ * For each token t:
+ *   p[e] = 1 / (1 + exp(-l[e])) with MOE_SCORE_SIGMOID, else
+ *          exp(l[e]) / sum over all E of exp(l)
+ *   s[e] = p[e] + bias[e]  (bias may be NULL: s = p)
+ *   A logit of -inf masks its expert: p = 0 and s = -inf, whatever the bias.
+ *   Groups (n_groups > topk_groups): the E experts form n_groups contiguous
+ *     groups; a group's score is its best s, or with MOE_GROUP_TOP2 the sum
+ *     of its two best (its only s when it has one expert); the best
+ *     topk_groups groups take part, ties to the lower group.
+ *   topk_idx = the k experts with the largest s among those, descending,
+ *     ties to the smaller id. A NaN s ranks below every other.
+ *   The order is that of s in exact arithmetic, to the resolution of 64-bit
+ *     floating point: where two scores lie closer than float32 resolves,
+ *     the token is ranked again in 64 bits.
+ *   topk_w[j] = scale * p[e_j] / sum_i p[e_i] with MOE_ROUTE_NORMALIZE, else
+ *     scale * p[e_j]; computed in float32. Masked experts, which are selected
+ *     only when too few others are left, get 0; a row whose selected scores
+ *     are all 0 gets zeros.
+ *   For a row that holds NaN or +inf under softmax, ids are distinct and in
+ *     range and nothing else is specified.
+ *
+ * Arguments:
+ *   logits   [T][E] float32, or bf16 with MOE_LOGITS_BF16; aligned to their
+ *            elements.
+ *   bias     [E] float32 or NULL.
+ *   n_groups, topk_groups  as moe_route_topk_grouped; 1, 1 for no groups.
+ *   scale    finite factor of the weights.
+ *   topk_idx [T][k] int32 out;  topk_w [T][k] float32 out.
+ * Errors: as moe_route_topk_grouped; MOE_ERR_INVALID_ARG for a scale that is
+ *   not finite.
+ */
+moe_status_t moe_route_scored(const void *logits, const float *bias, int64_t T, int32_t E,
+                              int32_t k, int32_t n_groups, int32_t topk_groups, float scale,
+                              uint32_t flags, int32_t *topk_idx, float *topk_w, void *stream);
+
+/*
+ * moe_route_scored_backward -- the gradient of moe_route_scored's weights
+ * with respect to the logits, given grad_w = dL/dtopk_w. The selection is
+ * not differentiated, so the bias gets no gradient. With g = grad_w, sums
+ * over the k selected:
+ *   softmax, normalised:  dl[e_j] = w_j (g_j - sum_i g_i w_i / scale)
+ *   sigmoid, normalised:  dl[e_j] = w_j (1 - p_j) (g_j - sum_i g_i w_i / scale)
+ *   sigmoid:              dl[e_j] = scale g_j p_j (1 - p_j)
+ *   softmax:              dl[e] = scale p_e ((g_j if e = e_j, else 0) - sum_i g_i p_i)
+ * and 0 for every other expert. Scores are recomputed from the logits.
+ *
+ * Arguments: logits, k, scale and flags as given to moe_route_scored
+ *   (MOE_GROUP_TOP2 has no effect on the gradient and is not accepted).
+ *   topk_idx  [T][k] int32, distinct within a row; ids outside [0, E) are
+ *             left out of the sums.
+ *   grad_w    [T][k] float32.
+ *   grad_logits [T][E] out, every element written, in the logits' type; must
+ *             not alias logits.
+ * Errors: as moe_route_scored.
+ */
+moe_status_t moe_route_scored_backward(const void *logits, const int32_t *topk_idx,
+                                       const float *grad_w, int64_t T, int32_t E, int32_t k,
+                                       float scale, uint32_t flags, void *grad_logits,
+                                       void *stream);
+
+/*
+ * moe_combine_backward -- the gradients of moe_combine_reduce's sum, given
+ * grad_out = dL/dout: for every kept replica
+ *   grad_y[pos[t][j]][h] = bf16( topk_w[t][j] * grad_out[t][h] )
+ *   grad_w[t][j]         = sum_h grad_out[t][h] * y[pos[t][j]][h]   (float32)
+ * and grad_w[t][j] = 0 for a dropped one. Rows of grad_y that no replica
+ * points at are not written. The gradients of shared and residual are
+ * grad_out itself.
+ *
+ * Defined by: as moe_combine_reduce, whose derivative this is.
+ *
+ * Arguments:
+ *   grad_out  [T][H] bf16, or float32 with MOE_COMBINE_OUT_FP32; 16-byte
+ *             aligned.
+ *   y         [y_rows][H] bf16, 16-byte aligned; NULL when grad_w is NULL.
+ *   pos       [T][k] int32, every row at most once; positions outside
+ *             [0, y_rows) count as dropped.
+ *   topk_w    [T][k] float32; NULL when grad_y is NULL.
+ *   grad_y    [y_rows][H] bf16 out, 16-byte aligned, or NULL.
+ *   grad_w    [T][k] float32 out, or NULL (not both NULL).
+ *   No output may alias an input.
+ * Errors: as moe_combine_reduce.
+ */
+moe_status_t moe_combine_backward(const void *grad_out, const uint16_t *y, int64_t y_rows,
+                                  const int32_t *pos, const float *topk_w, int64_t T, int32_t H,
+                                  int32_t k, uint32_t flags, uint16_t *grad_y, float *grad_w,
+                                  void *stream);
+
+/* activations of the experts' products */
+typedef enum moe_act {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,
+    MOE_ACT_SILU = 2,      /* z / (1 + exp(-z)) */
+    MOE_ACT_GELU = 3,      /* z (1 + erf(z / sqrt(2))) / 2 */
+    MOE_ACT_GELU_TANH = 4  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+} moe_act_t;
+
+/* moe_expert_product and moe_expert_product_dgrad flags */
+#define MOE_PRODUCT_GATED 1u  /* the activation of one half gates the other */
+
+/*
+ * moe_expert_product -- each local expert's linear map on its rows, with
+ * bias, activation, gate and residual applied before the one rounding:
+ *   z[i][o] = sum_h x[i][h] * W[l][o][h] + bias[l][o]     (row i of expert l)
+ *   y[i][o] = bf16( act(z[i][o]) + residual[i][o] ), or with
+ *             MOE_PRODUCT_GATED, where W and bias hold 2 O outputs per expert
+ *             (gate first),  bf16( act(z[i][o]) * z[i][O + o] + residual[i][o] )
+ *   pre[i]  = bf16(z[i]) where pre is given (what the backward pass reads).
+ * Products accumulate in float32 (MFMA); z stays in float32 until the
+ * result is rounded to nearest even.
+ *
+ * Rows are expert-major: expert l owns rows expert_offsets[l] to
+ * expert_offsets[l + 1], as moe_dispatch_layout (all experts local) and
+ * moe_recv_regroup_layout (local_expert_offsets) write them; an expert may
+ * have none. Rows from expert_offsets[E_l] on are neither read nor written.
+ * An always-active shared expert is E_l = 1 with offsets {0, T}.
+ *
+ * Defined by: "MoE All-to-All Dispatch and Ragged Routing", "Why MoE Token
+ * Dispatch is All-to-All" (a GPU computes its local experts on the rows it
+ * received) and "Fixed Capacity vs. Ragged Routing" (variable lengths).
+ *
+ * Arguments:
+ *   x         [max_rows][H] bf16.
+ *   expert_offsets [E_l + 1] int32 on the device, not decreasing, in
+ *             [0, max_rows]; values outside are clamped, so a broken
+ *             precondition computes wrong rows but accesses none outside.
+ *   W         [E_l][O][H] bf16 ([E_l][2 O][H] gated).
+ *   bias      [E_l][O] ([E_l][2 O]) bf16 or NULL.
+ *   residual  [max_rows][O] bf16 or NULL; may be y itself.
+ *   act       a moe_act value.
+ *   pre       [max_rows][O] ([max_rows][2 O]) bf16 out or NULL.
+ *   y         [max_rows][O] bf16 out.
+ *   Buffers are 16-byte aligned, expert_offsets 4-byte; outputs alias no
+ *   input but residual.
+ * Limits: 1 <= E_l <= 1024; H % 8 == 0, O % 8 == 0, both in [8, 65536];
+ *   max_rows < 2^31.
+ * Errors: MOE_ERR_INVALID_ARG (pointers, alignment, max_rows < 0, unknown act
+ *   or flags), MOE_ERR_UNSUPPORTED (limits).
+ */
+moe_status_t moe_expert_product(const uint16_t *x, const int32_t *expert_offsets, int32_t E_l,
+                                int64_t max_rows, int32_t H, int32_t O, const uint16_t *W,
+                                const uint16_t *bias, const uint16_t *residual, int32_t act,
+                                uint32_t flags, uint16_t *pre, uint16_t *y, void *stream);
+
+/*
+ * moe_expert_product_dgrad -- the gradient of a product with respect to its
+ * input, through the activation that made that input:
+ *   d[i][h] = sum_o grad_y[i][o] * W[l][o][h]              (row i of expert l)
+ *   pre NULL:  grad_x[i][h] = bf16( d[i][h] )
+ *   pre given: the input was act(pre); grad_x = bf16( d * act'(pre) )
+ *   MOE_PRODUCT_GATED: the input was act(pre[:, :H]) * pre[:, H:];
+ *     grad_x[i][h]     = bf16( d * pre[i][H + h] * act'(pre[i][h]) )
+ *     grad_x[i][H + h] = bf16( d * act(pre[i][h]) )
+ * With the pre of the product before it, grad_x is the gradient of that
+ * product's z, from which its own weight and input gradients follow.
+ *
+ * Arguments: as moe_expert_product; grad_y [max_rows][O] bf16,
+ *   W [E_l][O][H] bf16, pre [max_rows][H] ([max_rows][2 H] gated) bf16 or
+ *   NULL, grad_x [max_rows][H] ([max_rows][2 H] gated) bf16 out, which may be
+ *   pre itself. Rows from expert_offsets[E_l] on are neither read nor
+ *   written. Without pre, act must be MOE_ACT_NONE and flags 0.
+ * Errors: as moe_expert_product.
+ */
+moe_status_t moe_expert_product_dgrad(const uint16_t *grad_y, const int32_t *expert_offsets,
+                                      int32_t E_l, int64_t max_rows, int32_t O, int32_t H,
+                                      const uint16_t *W, const uint16_t *pre, int32_t act,
+                                      uint32_t flags, uint16_t *grad_x, void *stream);
+
+/* moe_expert_product_wgrad flags */
+#define MOE_GRAD_FP32 1u        /* grad_W is float32, else bf16 */
+#define MOE_GRAD_ACCUMULATE 2u  /* add to grad_W (float32 only) and grad_bias */
+
+/*
+ * moe_expert_product_wgrad -- the gradients of a product's weights and bias:
+ *   grad_W[l][o][h] = sum over expert l's rows i of grad_y[i][o] * x[i][h]
+ *   grad_bias[l][o] = sum over expert l's rows i of grad_y[i][o]
+ * accumulated in float32. Every element is written: an expert without rows
+ * gets zeros, or keeps what it had with MOE_GRAD_ACCUMULATE. For a gated
+ * product O is the 2 O of its forward call.
+ *
+ * Arguments: as moe_expert_product; grad_y [max_rows][O], x [max_rows][H]
+ *   bf16; grad_W [E_l][O][H] bf16 or float32 out; grad_bias [E_l][O] float32
+ *   out or NULL; workspace of moe_expert_product_wgrad_workspace_size()
+ *   bytes, 16-byte aligned, contents on entry do not matter (NULL when the
+ *   size is 0). Calls that overlap in time must not share a workspace.
+ * Errors: as moe_expert_product; MOE_ERR_INVALID_ARG for accumulation into
+ *   bf16; MOE_ERR_WORKSPACE.
+ */
+moe_status_t moe_expert_product_wgrad_workspace_size(int32_t E_l, int64_t max_rows, int32_t O,
+                                                     int32_t H, size_t *bytes);
+moe_status_t moe_expert_product_wgrad(const uint16_t *grad_y, const uint16_t *x,
+                                      const int32_t *expert_offsets, int32_t E_l,
+                                      int64_t max_rows, int32_t O, int32_t H, uint32_t flags,
+                                      void *grad_W, float *grad_bias, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
 /* moe_hbm_floor flags */
 #define MOE_FLOOR_NT_STORE 1u  /* stores carry the non-temporal hint */
 
