@@ -3,120 +3,162 @@
 // the activation's gradient) applied to the float32 sums before the one
 // rounding to bf16.
 //
-// Plain form: a block computes 64 rows of one expert by 64 columns (gated:
-// 32 gate columns and the 32 columns they gate), 4 x 4 sums per thread, with
-// operands staged through LDS in float32.
-#include "product_device.hpp"
+// A persistent block per CU takes tiles of 256 rows of one expert by 256
+// columns (gated: 128 gate columns and the 128 columns they gate, laid out
+// so that a lane holds both); product_gemm.hpp has the K loop.
+#include "product_gemm.hpp"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, kBM = 64, kBN = 64, kBK = 16;
-constexpr int kMaxBlocks = 2048;
+__device__ __forceinline__ f32x4 load_bf16x4(const uint16_t *p)
+{
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    return {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+}
+__device__ __forceinline__ void store_bf16x4(uint16_t *p, f32x4 v)
+{
+    uint2 o;
+    o.x = pack_bf16x2(v[0], v[1]);
+    o.y = pack_bf16x2(v[2], v[3]);
+    *reinterpret_cast<uint2 *>(p) = o;
+}
 
-// GRAD: B(n, k) = W[l][k][n], K = O; otherwise B(n, k) = W[l][n][k], K = H.
-// N: columns of the product's own output (O, or H for GRAD); PAIR: tile
-// column n < 32 is output n0 + n and column 32 + n the one it gates.
+struct ProductArgs {
+    const uint16_t *a;         // x, or grad_y (GRAD)
+    const int32_t *off;
+    const uint16_t *W, *bias, *residual, *pre_in;
+    uint16_t *pre_out, *out;
+    int32_t El, max_rows, K, N;  // N: columns before a gate doubles them
+};
+
+// four columns of one row, c a multiple of 4
 template <bool GRAD, bool GATED, int ACT>
-__global__ __launch_bounds__(kThreads) void product_kernel(
-    const uint16_t *__restrict__ a, const int32_t *__restrict__ off, int32_t El, int32_t max_rows,
-    int32_t K, int32_t N, const uint16_t *__restrict__ W, const uint16_t *__restrict__ bias,
-    const uint16_t *residual, const uint16_t *pre_in, uint16_t *pre_out, uint16_t *out)
+__device__ __forceinline__ void finish(const ProductArgs &p, int32_t l, int64_t row, int32_t c, f32x4 v, f32x4 g)
+{
+    const int64_t N = p.N;
+    if (GRAD) {
+        if (GATED) {
+            const f32x4 z = load_bf16x4(p.pre_in + row * 2 * N + c), u = load_bf16x4(p.pre_in + row * 2 * N + N + c);
+            f32x4 dz, du;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                dz[i] = v[i] * u[i] * act_grad<ACT>(z[i]);
+                du[i] = v[i] * act<ACT>(z[i]);
+            }
+            store_bf16x4(p.out + row * 2 * N + c, dz);
+            store_bf16x4(p.out + row * 2 * N + N + c, du);
+            return;
+        }
+        if (p.pre_in) {
+            const f32x4 z = load_bf16x4(p.pre_in + row * N + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] *= act_grad<ACT>(z[i]);
+        }
+        store_bf16x4(p.out + row * N + c, v);
+        return;
+    }
+    const int64_t wide = GATED ? 2 * N : N;
+    if (p.bias) {
+        v += load_bf16x4(p.bias + l * wide + c);
+        if (GATED)
+            g += load_bf16x4(p.bias + l * wide + N + c);
+    }
+    if (p.pre_out) {
+        store_bf16x4(p.pre_out + row * wide + c, v);
+        if (GATED)
+            store_bf16x4(p.pre_out + row * wide + N + c, g);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = GATED ? act<ACT>(v[i]) * g[i] : act<ACT>(v[i]);
+    if (p.residual)
+        v += load_bf16x4(p.residual + row * N + c);
+    store_bf16x4(p.out + row * N + c, v);
+}
+
+template <bool GRAD, bool GATED, int ACT>
+__global__ __launch_bounds__(kGemmThreads, 2) void product_kernel(ProductArgs p)
 {
     constexpr bool PAIR = GATED && !GRAD;
-    constexpr int kCols = PAIR ? kBN / 2 : kBN;
+    constexpr int kCols = PAIR ? kTile / 2 : kTile;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kGemmLdsBytes];
     __shared__ int32_t first[kMaxLocalExperts + 1];
-    __shared__ float As[kBK][kBM + 1], Bs[kBK][kBN + 1];
-    const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-    const int32_t row_tiles = plan_row_tiles<kThreads, kBM>(off, El, max_rows, first);
-    const int64_t nct = (N + kCols - 1) / kCols;
-    const int64_t wide = PAIR ? 2 * (int64_t)N : N;
-    for (int64_t u = blockIdx.x; u < row_tiles * nct; u += gridDim.x) {
+    const int32_t row_tiles = plan_row_tiles<kGemmThreads, kTile>(p.off, p.El, p.max_rows, first);
+    const int64_t nct = (p.N + kCols - 1) / kCols;
+    const int64_t wide = PAIR ? 2 * (int64_t)p.N : p.N;
+    const int nk = (p.K + kTileK - 1) / kTileK;
+    Gemm<false, GRAD> gemm;
+    gemm.init_lane();
+    // each XCD (blockIdx % 8) takes runs of consecutive tiles
+    const int32_t per_xcd = gridDim.x / 8;
+    const int64_t slot = gridDim.x % 8 ? blockIdx.x : (int64_t)(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
+    for (int64_t u = slot; u < row_tiles * nct; u += gridDim.x) {
         const int32_t rt = (int32_t)(u / nct), n0 = (int32_t)(u % nct) * kCols;
-        const int32_t l = tile_expert(first, El, rt);
-        const Rows r = expert_rows(off, l, max_rows);
-        const int64_t row0 = r.begin + (int64_t)(rt - first[l]) * kBM;
-        const int rows = (int)min((int64_t)kBM, r.end - row0);
-        const uint16_t *Wl = W + (int64_t)l * wide * K;
-        float acc[4][4] = {};
-        for (int32_t k0 = 0; k0 < K; k0 += kBK) {
-            for (int i = tid; i < kBM * kBK; i += kThreads) {
-                const int m = i / kBK, k = i % kBK;
-                As[k][m] = m < rows && k0 + k < K ? bf16_to_f32(a[(row0 + m) * K + k0 + k]) : 0.f;
-                const int n = m;
-                const int32_t col = PAIR ? n0 + n % 32 : n0 + n;
-                const int64_t wrow = PAIR && n >= 32 ? (int64_t)N + col : col;
-                float b = 0.f;
-                if (col < N && k0 + k < K)
-                    b = bf16_to_f32(GRAD ? Wl[(int64_t)(k0 + k) * N + col] : Wl[wrow * K + k0 + k]);
-                Bs[k][n] = b;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < kBK; ++k) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[i][j] = fmaf(As[k][ty * 4 + i], Bs[k][(j / 2) * 32 + tx * 2 + j % 2], acc[i][j]);
-            }
-            __syncthreads();
+        const int32_t l = __builtin_amdgcn_readfirstlane(tile_expert(first, p.El, rt));
+        const Rows r = expert_rows(p.off, l, p.max_rows);
+        const int32_t row0 = __builtin_amdgcn_readfirstlane(r.begin + (rt - first[l]) * kTile);
+        const int32_t rows = __builtin_amdgcn_readfirstlane(min(kTile, r.end - row0));
+        if (rows <= 0)
+            continue;
+        gemm.A.init(p.a + (int64_t)row0 * p.K, rows, p.K, gemm.wave, gemm.lane, 128, [](int j) { return j * 8; });
+        const uint16_t *Wl = p.W + (int64_t)l * wide * p.K;
+        if constexpr (GRAD) {
+            gemm.B.init_strided(Wl + n0, p.K, p.N, p.N - n0, gemm.wave, gemm.lane);
+        } else if constexpr (GATED) {
+            // rows of a half: for each wave's 32 columns, 16 gate then 16 up
+            const bool up = (gemm.wave >> 1) & 1;
+            gemm.B.init(Wl + ((up ? (int64_t)p.N : 0) + n0) * p.K, p.N - n0, p.K, gemm.wave, gemm.lane, 64,
+                        [](int j) { return (j >> 2) * 16 + (j & 1) * 8; });
+        } else {
+            gemm.B.init(Wl + (int64_t)n0 * p.K, p.N - n0, p.K, gemm.wave, gemm.lane, 128, [](int j) { return j * 8; });
         }
-        for (int i = 0; i < 4; ++i) {
-            const int m = ty * 4 + i;
-            if (m >= rows)
-                continue;
-            const int64_t row = row0 + m;
-            for (int j = 0; j < (PAIR ? 2 : 4); ++j) {
-                const int32_t c = n0 + (j / 2) * 32 + tx * 2 + j % 2;
-                if (c >= N)
+        Acc acc;
+        gemm.start(lds, nk);
+        gemm.run(lds, nk, acc);
+#pragma unroll
+        for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int32_t m = ha * 128 + gemm.wm * 64 + i * 16 + (gemm.lane & 15);
+                if (m >= rows)
                     continue;
-                float v = acc[i][j];
-                if (GRAD) {
-                    if (GATED) {
-                        const float g = bf16_to_f32(pre_in[row * 2 * N + c]);
-                        const float up = bf16_to_f32(pre_in[row * 2 * N + N + c]);
-                        out[row * 2 * N + c] = f32_to_bf16(v * up * act_grad<ACT>(g));
-                        out[row * 2 * N + N + c] = f32_to_bf16(v * act<ACT>(g));
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb) {
+                    if (PAIR) {
+                        const int32_t c = n0 + hb * 64 + gemm.wn * 16 + (gemm.lane >> 4) * 4;
+                        if (c < p.N)
+                            finish<GRAD, GATED, ACT>(p, l, (int64_t)row0 + m, c, acc[ha][hb][i][0], acc[ha][hb][i][1]);
                     } else {
-                        if (pre_in)
-                            v *= act_grad<ACT>(bf16_to_f32(pre_in[row * N + c]));
-                        out[row * N + c] = f32_to_bf16(v);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int32_t c = n0 + hb * 128 + gemm.wn * 32 + j * 16 + (gemm.lane >> 4) * 4;
+                            if (c < p.N)
+                                finish<GRAD, GATED, ACT>(p, l, (int64_t)row0 + m, c, acc[ha][hb][i][j], f32x4{});
+                        }
                     }
-                    continue;
                 }
-                if (bias)
-                    v += bf16_to_f32(bias[l * wide + c]);
-                if (pre_out)
-                    pre_out[row * wide + c] = f32_to_bf16(v);
-                v = act<ACT>(v);
-                if (PAIR) {
-                    float g = acc[i][j + 2];
-                    if (bias)
-                        g += bf16_to_f32(bias[l * wide + N + c]);
-                    if (pre_out)
-                        pre_out[row * wide + N + c] = f32_to_bf16(g);
-                    v *= g;
-                }
-                if (residual)
-                    v += bf16_to_f32(residual[row * N + c]);
-                out[row * N + c] = f32_to_bf16(v);
             }
-        }
+        wait_loads<0>();
+        slot_end();
     }
 }
 
 template <bool GRAD>
-hipError_t launch(const uint16_t *a, const int32_t *off, int32_t El, int64_t max_rows, int32_t K,
-                  int32_t N, const uint16_t *W, const uint16_t *bias, const uint16_t *residual,
-                  const uint16_t *pre_in, int32_t act, bool gated, uint16_t *pre_out, uint16_t *out,
-                  hipStream_t stream)
+hipError_t launch(const ProductArgs &p, int32_t act, bool gated, hipStream_t stream)
 {
-    const int64_t tiles = (max_rows / kBM + El) * ((N + 31) / 32);
-    const dim3 grid((unsigned)(tiles < kMaxBlocks ? tiles : kMaxBlocks));
-#define MOE_PRODUCT_LAUNCH(G, A)                                                                    \
-    hipLaunchKernelGGL((product_kernel<GRAD, G, A>), grid, dim3(kThreads), 0, stream, a, off, El,   \
-                       (int32_t)max_rows, K, N, W, bias, residual, pre_in, pre_out, out);           \
+    int device = 0, cus = 0;
+    hipError_t err = hipGetDevice(&device);
+    if (err == hipSuccess)
+        err = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
+    if (err != hipSuccess)
+        return err;
+    const int kCols = gated && !GRAD ? kTile / 2 : kTile;
+    const int64_t tiles = ((int64_t)p.max_rows / kTile + p.El) * ((p.N + kCols - 1) / kCols);
+    const dim3 grid((unsigned)(tiles < cus ? tiles : cus));
+#define MOE_PRODUCT_LAUNCH(G, A)                                                                 \
+    hipLaunchKernelGGL((product_kernel<GRAD, G, A>), grid, dim3(kGemmThreads), 0, stream, p);    \
     return hipGetLastError()
 #define MOE_PRODUCT_ACT(A)                \
     case A:                               \
@@ -145,8 +187,8 @@ hipError_t launch_expert_product(const uint16_t *x, const int32_t *off, int32_t 
                                  const uint16_t *bias, const uint16_t *residual, int32_t act,
                                  bool gated, uint16_t *pre, uint16_t *y, hipStream_t stream)
 {
-    return launch<false>(x, off, El, max_rows, H, O, W, bias, residual, nullptr, act, gated, pre, y,
-                         stream);
+    const ProductArgs p = {x, off, W, bias, residual, nullptr, pre, y, El, (int32_t)max_rows, H, O};
+    return launch<false>(p, act, gated, stream);
 }
 
 hipError_t launch_expert_dgrad(const uint16_t *grad_y, const int32_t *off, int32_t El,
@@ -154,8 +196,8 @@ hipError_t launch_expert_dgrad(const uint16_t *grad_y, const int32_t *off, int32
                                const uint16_t *pre, int32_t act, bool gated, uint16_t *grad_x,
                                hipStream_t stream)
 {
-    return launch<true>(grad_y, off, El, max_rows, O, H, W, nullptr, nullptr, pre, act, gated,
-                        nullptr, grad_x, stream);
+    const ProductArgs p = {grad_y, off, W, nullptr, nullptr, pre, nullptr, grad_x, El, (int32_t)max_rows, O, H};
+    return launch<true>(p, act, gated, stream);
 }
 
 }  // namespace moe

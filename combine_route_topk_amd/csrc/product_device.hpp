@@ -21,7 +21,8 @@ __device__ __forceinline__ Rows expert_rows(const int32_t *__restrict__ off, int
 }
 
 // first[l] = row tiles of BM rows before expert l, for l <= El (El <= 1024);
-// returns their total. Every thread of the block takes part; `first` is in
+// returns their total, or 0 where the offsets decrease (otherwise the experts'
+// rows are disjoint, and the total at most max_rows / BM + El). Every thread of the block takes part; `first` is in
 // LDS and ready after the call. One pass over at most 1025 offsets by the
 // block itself costs a launch less than a table written by another kernel.
 template <int THREADS, int BM>
@@ -31,8 +32,10 @@ __device__ int32_t plan_row_tiles(const int32_t *__restrict__ off, int32_t El, i
     constexpr int PER = (kMaxLocalExperts + THREADS - 1) / THREADS;
     constexpr int WAVES = THREADS / kWave;
     __shared__ int32_t wave_total[WAVES];
+    __shared__ bool wave_bad[WAVES];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave;
     int32_t n[PER], part = 0;
+    bool bad = false;
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
         const int l = tid * PER + u;
@@ -40,12 +43,16 @@ __device__ int32_t plan_row_tiles(const int32_t *__restrict__ off, int32_t El, i
         if (l < El) {
             const Rows r = expert_rows(off, l, max_rows);
             n[u] = (int32_t)(((int64_t)r.end - r.begin + BM - 1) / BM);
+            bad |= off[l + 1] < off[l];
         }
         part += n[u];
     }
     const int32_t inc = wave_inclusive_sum(part);
-    if (lane == kWave - 1)
+    const uint64_t any_bad = ballot64(bad);
+    if (lane == kWave - 1) {
         wave_total[w] = inc;
+        wave_bad[w] = any_bad != 0;
+    }
     __syncthreads();
     int32_t run = inc - part, all = 0;
 #pragma unroll
@@ -53,6 +60,10 @@ __device__ int32_t plan_row_tiles(const int32_t *__restrict__ off, int32_t El, i
         run += u < w ? wave_total[u] : 0;
         all += wave_total[u];
     }
+    bad = false;
+#pragma unroll
+    for (int u = 0; u < WAVES; ++u)
+        bad |= wave_bad[u];
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
         const int l = tid * PER + u;
@@ -63,7 +74,7 @@ __device__ int32_t plan_row_tiles(const int32_t *__restrict__ off, int32_t El, i
     if (tid == 0)
         first[El] = all;
     __syncthreads();
-    return all;
+    return bad ? 0 : all;
 }
 
 // the expert whose tiles hold tile t: the largest l with first[l] <= t

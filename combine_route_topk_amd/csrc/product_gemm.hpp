@@ -1,0 +1,371 @@
+// product_gemm.hpp -- the MFMA core of the experts' products and of their
+// gradients: one 256 x 256 tile of C = A B^T, summed over K in float32.
+//
+// Bound. At 256 x 256 x 64 a K-tile moves 64 KiB into LDS for 8.4 MFLOP, so
+// the matrix units bound it as long as they are never left waiting: 8 waves,
+// two on each SIMD, compute 128 x 64 each in 16 x 16 x 32 MFMAs (128
+// accumulator registers).
+//
+// Schedule. A wave's K-tile is four phases of 16 MFMAs, one for each pair of
+// halves of A's rows and B's columns. Waves 0-3 and waves 4-7 run half a
+// phase apart, held so by barriers: while one of a SIMD's two waves issues
+// MFMAs the other reads the fragments of its next phase from LDS and starts
+// the loads of later K-tiles, so the matrix unit always has a wave that is
+// ready. Operands go from memory straight to LDS in half tiles of 16 KiB, one
+// per phase, into two stages (128 KiB); each half tile is started as soon as
+// every wave has read the one it replaces, six phases before it is read, so
+// a wait never drains the queue: five half tiles stay in flight across it.
+//
+// Operands. K-contiguous (rows of x, grad_y and a forward W): LDS holds 128
+// rows of 64 k, and a fragment is one 16-byte read per lane. K-strided (W in
+// the input gradient; both operands of the weight gradient): LDS holds 64
+// k-rows of 128 columns, and a fragment is two transposing reads. In both the
+// 16-byte pieces of a row are permuted by the row's number so that the lanes
+// of a read fall into different banks. Buffer descriptors end where the
+// operand ends, and reads past that end give zeros: rows past an expert's
+// last, columns past the width and the tail of K cost no branch.
+#pragma once
+
+#include "product_device.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kGemmThreads = 512;
+constexpr int kTile = 256, kTileK = 64;
+constexpr int kHalfBytes = 128 * kTileK * 2;   // half an operand's tile
+constexpr int kStageBytes = 4 * kHalfBytes;    // A half 0, A half 1, B half 0, B half 1
+constexpr int kGemmLdsBytes = 2 * kStageBytes;
+constexpr int kGemmBufferFlags = 0x00020000;   // raw byte-addressed buffer
+constexpr uint32_t kOutside = 0x80000000u;     // an offset past every descriptor's end
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// One operand of a tile: 256 rows (of A) or columns (of B), by K.
+template <bool STRIDED>
+struct Operand {
+    const uint8_t *base;  // first row's (column's) element of K = 0
+    int64_t bytes;        // from base to the operand's end (STRIDED)
+    int64_t kstep;        // bytes from one K-tile to the next (STRIDED)
+    uint32_t records;     // descriptor size (K-contiguous)
+    uint32_t off[2][2];   // this lane's byte offset in load i of half h
+    uint32_t tail;        // kOutside where this lane's piece lies past K in the last K-tile
+
+    // K-contiguous: `rows` valid rows of K elements from p. half_rows: rows
+    // between the halves (128, or 64 of a gated W whose halves hold 64 gate
+    // and 64 up columns); row_of: row of load index j within a half.
+    template <class RowOf>
+    __device__ __forceinline__ void init(const uint16_t *p, int64_t rows, int32_t K, int wave, int lane,
+                                         int half_rows, RowOf row_of)
+    {
+        static_assert(!STRIDED, "");
+        base = reinterpret_cast<const uint8_t *>(p);
+        records = (uint32_t)(max(min(rows, (int64_t)kTile), (int64_t)0) * K * 2);
+        const int c = (lane & 7) ^ (lane >> 3);  // piece at LDS position lane % 8 of row lane / 8
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                off[h][i] = (uint32_t)(h * half_rows + row_of(i * 8 + wave) + (lane >> 3)) * (uint32_t)K * 2u + c * 16;
+        tail = (K & (kTileK - 1)) && c * 8 >= (K & (kTileK - 1)) ? kOutside : 0u;
+    }
+
+    // K-strided: element (k, n) at p[k * ld + n], K rows, n < width.
+    __device__ __forceinline__ void init_strided(const uint16_t *p, int64_t K, int32_t ld, int32_t width, int wave,
+                                                 int lane)
+    {
+        base = reinterpret_cast<const uint8_t *>(p);
+        // the last row ends at its valid width: rows K and later lie past it
+        bytes = K > 0 ? ((K - 1) * ld + width) * 2 : 0;
+        kstep = (int64_t)kTileK * ld * 2;
+        const int kr = lane >> 4, swz = (kr & 3) | (((wave >> 1) & 1) << 2);
+        const int c = (lane & 15) ^ (2 * swz);  // piece at LDS position lane % 16
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                off[h][i] = h * 128 + c * 8 >= width
+                                ? kOutside
+                                : (uint32_t)((i * 8 + wave) * 4 + kr) * (uint32_t)ld * 2u + h * 256 + c * 16;
+        tail = 0;
+    }
+
+    // start the loads of half h of K-tile t (of nk) into LDS at dst
+    __device__ __forceinline__ void load(uint8_t *__restrict__ dst, int h, int t, int nk, int wave) const
+    {
+        if (STRIDED) {
+            const int64_t at = (int64_t)t * kstep;
+            const int64_t left = t < nk ? bytes - at : 0;
+            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<uint8_t *>(base + at), 0, (uint32_t)min(max(left, (int64_t)0), (int64_t)0x7FFFFFFF),
+                kGemmBufferFlags);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst + (i * 8 + wave) * 1024, 16, off[h][i], 0, 0, 0);
+        } else {
+            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<uint8_t *>(base), 0, t < nk ? records : 0u, kGemmBufferFlags);
+            const uint32_t cut = t == nk - 1 ? tail : 0u;
+            // the descriptor's end is checked less the scalar offset, which must not pass it
+            const uint32_t k0 = t < nk ? t * (kTileK * 2) : 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst + (i * 8 + wave) * 1024, 16, off[h][i] | cut,
+                                                         k0, 0, 0);
+        }
+    }
+};
+
+// Fragment reads. They are written as instructions, each block with its own
+// wait, because the compiler takes every LDS read to depend on every load into
+// LDS in flight and would drain the queue before each; the schedule orders
+// them with barriers and counted waits instead. LDS addresses are byte
+// offsets in 32 bits.
+__device__ __forceinline__ uint32_t lds_offset(const uint8_t *p)
+{
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)p;
+}
+
+// Lane L's address within a half tile of its part of fragment f (rows or
+// columns first + 16 f), for k = kk * 32 + (L / 16) * 8 .. + 7.
+__device__ __forceinline__ uint32_t frag_row(int first, int kk, int lane)
+{
+    const int i = lane & 15, g = lane >> 4;
+    return (uint32_t)((first + i) * 128 + (((kk * 4 + g) ^ (i & 7)) << 4));
+}
+__device__ __forceinline__ uint32_t frag_strided(int first, int f, int lane)
+{
+    const int i = lane & 15, g = lane >> 4, swz = (i >> 2) | ((g & 1) << 2);
+    return (uint32_t)((g * 8 + (i >> 2)) * 256 + (((first / 16 + f) ^ swz) << 5) + (i & 3) * 8);
+}
+
+__device__ __forceinline__ bf16x8 join(s16x4 lo, s16x4 hi)
+{
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// four fragments of 16 rows each, both halves of a K-tile
+struct FragA {
+    bf16x8 v[2][4];
+};
+// two fragments of 16 columns each
+struct FragB {
+    bf16x8 v[2][2];
+};
+
+template <bool STRIDED>
+struct AddrA {
+    uint32_t a[STRIDED ? 4 : 2];
+    __device__ __forceinline__ void init(int first, int lane)
+    {
+#pragma unroll
+        for (int f = 0; f < (STRIDED ? 4 : 2); ++f)
+            a[f] = STRIDED ? frag_strided(first, f, lane) : frag_row(first, f, lane);
+    }
+    __device__ __forceinline__ void read(uint32_t half, FragA &r) const
+    {
+        if constexpr (STRIDED) {
+            s16x4 q[2][4][2];
+            asm volatile("ds_read_b64_tr_b16 %0, %16\n\tds_read_b64_tr_b16 %1, %16 offset:1024\n\t"
+                         "ds_read_b64_tr_b16 %2, %17\n\tds_read_b64_tr_b16 %3, %17 offset:1024\n\t"
+                         "ds_read_b64_tr_b16 %4, %18\n\tds_read_b64_tr_b16 %5, %18 offset:1024\n\t"
+                         "ds_read_b64_tr_b16 %6, %19\n\tds_read_b64_tr_b16 %7, %19 offset:1024\n\t"
+                         "ds_read_b64_tr_b16 %8, %16 offset:8192\n\tds_read_b64_tr_b16 %9, %16 offset:9216\n\t"
+                         "ds_read_b64_tr_b16 %10, %17 offset:8192\n\tds_read_b64_tr_b16 %11, %17 offset:9216\n\t"
+                         "ds_read_b64_tr_b16 %12, %18 offset:8192\n\tds_read_b64_tr_b16 %13, %18 offset:9216\n\t"
+                         "ds_read_b64_tr_b16 %14, %19 offset:8192\n\tds_read_b64_tr_b16 %15, %19 offset:9216\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(q[0][0][0]), "=&v"(q[0][0][1]), "=&v"(q[0][1][0]), "=&v"(q[0][1][1]),
+                           "=&v"(q[0][2][0]), "=&v"(q[0][2][1]), "=&v"(q[0][3][0]), "=&v"(q[0][3][1]),
+                           "=&v"(q[1][0][0]), "=&v"(q[1][0][1]), "=&v"(q[1][1][0]), "=&v"(q[1][1][1]),
+                           "=&v"(q[1][2][0]), "=&v"(q[1][2][1]), "=&v"(q[1][3][0]), "=&v"(q[1][3][1])
+                         : "v"(half + a[0]), "v"(half + a[1]), "v"(half + a[2]), "v"(half + a[3])
+                         : "memory");
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+                    r.v[kk][f] = join(q[kk][f][0], q[kk][f][1]);
+        } else {
+            asm volatile("ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:2048\n\t"
+                         "ds_read_b128 %2, %8 offset:4096\n\tds_read_b128 %3, %8 offset:6144\n\t"
+                         "ds_read_b128 %4, %9\n\tds_read_b128 %5, %9 offset:2048\n\t"
+                         "ds_read_b128 %6, %9 offset:4096\n\tds_read_b128 %7, %9 offset:6144\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(r.v[0][0]), "=&v"(r.v[0][1]), "=&v"(r.v[0][2]), "=&v"(r.v[0][3]),
+                           "=&v"(r.v[1][0]), "=&v"(r.v[1][1]), "=&v"(r.v[1][2]), "=&v"(r.v[1][3])
+                         : "v"(half + a[0]), "v"(half + a[1])
+                         : "memory");
+        }
+    }
+};
+
+template <bool STRIDED>
+struct AddrB {
+    uint32_t a[2];
+    __device__ __forceinline__ void init(int first, int lane)
+    {
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+            a[f] = STRIDED ? frag_strided(first, f, lane) : frag_row(first, f, lane);
+    }
+    __device__ __forceinline__ void read(uint32_t half, FragB &r) const
+    {
+        if constexpr (STRIDED) {
+            s16x4 q[2][2][2];
+            asm volatile("ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %8 offset:1024\n\t"
+                         "ds_read_b64_tr_b16 %2, %9\n\tds_read_b64_tr_b16 %3, %9 offset:1024\n\t"
+                         "ds_read_b64_tr_b16 %4, %8 offset:8192\n\tds_read_b64_tr_b16 %5, %8 offset:9216\n\t"
+                         "ds_read_b64_tr_b16 %6, %9 offset:8192\n\tds_read_b64_tr_b16 %7, %9 offset:9216\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(q[0][0][0]), "=&v"(q[0][0][1]), "=&v"(q[0][1][0]), "=&v"(q[0][1][1]),
+                           "=&v"(q[1][0][0]), "=&v"(q[1][0][1]), "=&v"(q[1][1][0]), "=&v"(q[1][1][1])
+                         : "v"(half + a[0]), "v"(half + a[1])
+                         : "memory");
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    r.v[kk][f] = join(q[kk][f][0], q[kk][f][1]);
+        } else {
+            asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:2048\n\t"
+                         "ds_read_b128 %2, %5\n\tds_read_b128 %3, %5 offset:2048\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(r.v[0][0]), "=&v"(r.v[0][1]), "=&v"(r.v[1][0]), "=&v"(r.v[1][1])
+                         : "v"(half + a[0]), "v"(half + a[1])
+                         : "memory");
+        }
+    }
+};
+
+// wait until at most N of this wave's vector-memory operations are outstanding
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+__device__ __forceinline__ void slot_end()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// acc[hA][hB][fa][fb]: lane L holds row hA * 128 + wm * 64 + fa * 16 + L % 16
+// and columns hB * 128 + wn * 32 + fb * 16 + (L / 16) * 4 + 0..3 (of the tile
+// as it lies in LDS).
+typedef f32x4 Acc[2][2][4][2];
+
+template <bool ASTR, bool BSTR>
+struct Gemm {
+    Operand<ASTR> A;
+    Operand<BSTR> B;
+    AddrA<ASTR> fa;
+    AddrB<BSTR> fb;
+    int wave, lane, wm, wn;
+
+    __device__ __forceinline__ void init_lane()
+    {
+        lane = threadIdx.x & (kWave - 1);
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        wm = wave >> 2;
+        wn = wave & 3;
+        fa.init(wm * 64, lane);
+        fb.init(wn * 32, lane);
+    }
+
+    // the loads that run ahead of the first phase, in the order they are waited for
+    __device__ __forceinline__ void start(uint8_t *lds, int nk) const
+    {
+        uint8_t *s0 = lds, *s1 = lds + kStageBytes;
+        B.load(s0 + 2 * kHalfBytes, 0, 0, nk, wave);
+        A.load(s0, 0, 0, nk, wave);
+        B.load(s0 + 3 * kHalfBytes, 1, 0, nk, wave);
+        A.load(s0 + kHalfBytes, 1, 0, nk, wave);
+        B.load(s1 + 2 * kHalfBytes, 0, 1, nk, wave);
+        A.load(s1, 0, 1, nk, wave);
+        B.load(s1 + 3 * kHalfBytes, 1, 1, nk, wave);
+    }
+
+    __device__ __forceinline__ static void mfmas(const FragA &a, const FragB &b, f32x4 (&c)[4][2])
+    {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    c[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[kk][j], a.v[kk][i], c[i][j], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
+    }
+
+    // K-tile t, which lies in stage `cur`. A slot between two barriers holds
+    // either reads and load starts or MFMAs; each half tile is read by the last
+    // wave, and waited for, a barrier before its refill is started.
+    __device__ __forceinline__ void ktile(uint8_t *cur, uint8_t *other, int t, int nk, Acc &acc) const
+    {
+        const uint32_t at = lds_offset(cur);
+        FragA a;
+        FragB bl, bh;
+        // phase 0
+        A.load(other + kHalfBytes, 1, t + 1, nk, wave);
+        fb.read(at + 2 * kHalfBytes, bl);
+        fa.read(at, a);
+        wait_loads<10>();
+        slot_end();
+        mfmas(a, bl, acc[0][0]);
+        slot_end();
+        // phase 1
+        B.load(cur + 2 * kHalfBytes, 0, t + 2, nk, wave);
+        fb.read(at + 3 * kHalfBytes, bh);
+        wait_loads<10>();
+        slot_end();
+        mfmas(a, bh, acc[0][1]);
+        slot_end();
+        // phase 2
+        A.load(cur, 0, t + 2, nk, wave);
+        fa.read(at + kHalfBytes, a);
+        slot_end();
+        mfmas(a, bh, acc[1][1]);
+        slot_end();
+        // phase 3
+        B.load(cur + 3 * kHalfBytes, 1, t + 2, nk, wave);
+        wait_loads<10>();
+        slot_end();
+        mfmas(a, bl, acc[1][0]);
+        slot_end();
+    }
+
+    // The whole K loop; start() has been called. On return every wave has read
+    // what it needs of LDS, and the loads still in flight bring only zeros.
+    __device__ __forceinline__ void run(uint8_t *lds, int nk, Acc &acc) const
+    {
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                acc[q >> 3][(q >> 2) & 1][q & 3][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        uint8_t *s0 = lds, *s1 = lds + kStageBytes;
+        wait_loads<10>();
+        slot_end();
+        if (wm)  // the second group of waves starts half a phase later
+            slot_end();
+        int t = 0;
+        for (; t + 1 < nk; t += 2) {
+            ktile(s0, s1, t, nk, acc);
+            ktile(s1, s0, t + 1, nk, acc);
+        }
+        if (t < nk)
+            ktile(s0, s1, t, nk, acc);
+        if (!wm)
+            slot_end();
+    }
+};
+
+}  // namespace
+}  // namespace moe

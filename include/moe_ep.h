@@ -677,8 +677,9 @@ typedef enum moe_act {
  * Arguments:
  *   x         [max_rows][H] bf16.
  *   expert_offsets [E_l + 1] int32 on the device, not decreasing, in
- *             [0, max_rows]; values outside are clamped, so a broken
- *             precondition computes wrong rows but accesses none outside.
+ *             [0, max_rows]. Values outside are clamped and nothing is
+ *             computed where they decrease, so a broken precondition
+ *             accesses no row outside the buffers.
  *   W         [E_l][O][H] bf16 ([E_l][2 O][H] gated).
  *   bias      [E_l][O] ([E_l][2 O]) bf16 or NULL.
  *   residual  [max_rows][O] bf16 or NULL; may be y itself.
