@@ -1,68 +1,88 @@
 // product_wgrad.hip -- the gradients of the experts' weights and biases:
 // grad_W[l] = grad_y[rows of l]^T x[rows of l], summed over the rows in
-// float32.
-//
-// Plain form: a block computes 64 x 64 of one expert's grad_W, 4 x 4 sums
-// per thread, with operands staged through LDS in float32.
-#include "product_device.hpp"
+// float32. Both operands are K-strided (K is the rows); product_gemm.hpp has
+// the K loop. grad_bias is summed by a kernel of its own.
+#include "product_gemm.hpp"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, kBM = 64, kBN = 64, kBK = 16;
-constexpr int kMaxBlocks = 2048;
+struct WgradArgs {
+    const uint16_t *gy, *x;
+    const int32_t *off;
+    void *gW;
+    int32_t El, max_rows, O, H;
+};
 
 template <bool FP32, bool ACCUMULATE>
-__global__ __launch_bounds__(kThreads) void wgrad_kernel(
-    const uint16_t *__restrict__ gy, const uint16_t *__restrict__ x, const int32_t *__restrict__ off,
-    int32_t El, int32_t max_rows, int32_t O, int32_t H, void *__restrict__ gW, float *__restrict__ gb)
+__global__ __launch_bounds__(kGemmThreads, 2) void wgrad_kernel(WgradArgs p)
 {
-    __shared__ float As[kBK][kBM + 1], Bs[kBK][kBN + 1];
-    const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-    const int64_t nh = (H + kBN - 1) / kBN, no = (O + kBM - 1) / kBM;
-    for (int64_t u = blockIdx.x; u < El * no * nh; u += gridDim.x) {
-        const int32_t h0 = (int32_t)(u % nh) * kBN, o0 = (int32_t)(u / nh % no) * kBM;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kGemmLdsBytes];
+    const int64_t no = (p.O + kTile - 1) / kTile, nh = (p.H + kTile - 1) / kTile;
+    Gemm<true, true> gemm;
+    gemm.init_lane();
+    const int32_t per_xcd = gridDim.x / 8;
+    const int64_t slot = gridDim.x % 8 ? blockIdx.x : (int64_t)(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
+    for (int64_t u = slot; u < p.El * no * nh; u += gridDim.x) {
+        const int32_t h0 = (int32_t)(u % nh) * kTile, o0 = (int32_t)(u / nh % no) * kTile;
         const int32_t l = (int32_t)(u / (nh * no));
-        const Rows r = expert_rows(off, l, max_rows);
-        float acc[4][4] = {}, bsum = 0.f;
-        for (int64_t k0 = r.begin; k0 < r.end; k0 += kBK) {
-            for (int i = tid; i < kBM * kBK; i += kThreads) {
-                const int k = i / kBM, m = i % kBM;
-                const bool in = k0 + k < r.end;
-                As[k][m] = in && o0 + m < O ? bf16_to_f32(gy[(k0 + k) * O + o0 + m]) : 0.f;
-                Bs[k][m] = in && h0 + m < H ? bf16_to_f32(x[(k0 + k) * H + h0 + m]) : 0.f;
-            }
-            __syncthreads();
+        const Rows r = expert_rows(p.off, l, p.max_rows);
+        const int32_t begin = __builtin_amdgcn_readfirstlane(r.begin);
+        const int32_t n = __builtin_amdgcn_readfirstlane(r.end - r.begin);
+        const int nk = (n + kTileK - 1) / kTileK;
+        gemm.A.init_strided(p.gy + (int64_t)begin * p.O + o0, n, p.O, p.O - o0, gemm.wave, gemm.lane);
+        gemm.B.init_strided(p.x + (int64_t)begin * p.H + h0, n, p.H, p.H - h0, gemm.wave, gemm.lane);
+        Acc acc;
+        gemm.start(lds, nk);
+        gemm.run(lds, nk, acc);
 #pragma unroll
-            for (int k = 0; k < kBK; ++k) {
+        for (int ha = 0; ha < 2; ++ha)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[i][j] = fmaf(As[k][ty * 4 + i], Bs[k][tx * 4 + j], acc[i][j]);
-                if (tid < kBM)
-                    bsum += As[k][tid];
-            }
-            __syncthreads();
-        }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int32_t o = o0 + ty * 4 + i, h = h0 + tx * 4 + j;
-                if (o >= O || h >= H)
+            for (int i = 0; i < 4; ++i) {
+                const int32_t o = o0 + ha * 128 + gemm.wm * 64 + i * 16 + (gemm.lane & 15);
+                if (o >= p.O)
                     continue;
-                const int64_t at = ((int64_t)l * O + o) * H + h;
-                if (FP32) {
-                    float *p = static_cast<float *>(gW) + at;
-                    *p = ACCUMULATE ? *p + acc[i][j] : acc[i][j];
-                } else {
-                    static_cast<uint16_t *>(gW)[at] = f32_to_bf16(acc[i][j]);
-                }
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int32_t h = h0 + hb * 128 + gemm.wn * 32 + j * 16 + (gemm.lane >> 4) * 4;
+                        if (h >= p.H)
+                            continue;
+                        const int64_t at = ((int64_t)l * p.O + o) * p.H + h;
+                        f32x4 v = acc[ha][hb][i][j];
+                        if (FP32) {
+                            f32x4 *q = reinterpret_cast<f32x4 *>(static_cast<float *>(p.gW) + at);
+                            if (ACCUMULATE)
+                                v += *q;
+                            *q = v;
+                        } else {
+                            uint2 b;
+                            b.x = pack_bf16x2(v[0], v[1]);
+                            b.y = pack_bf16x2(v[2], v[3]);
+                            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.gW) + at) = b;
+                        }
+                    }
             }
-        if (gb && h0 == 0 && tid < kBM && o0 + tid < O) {
-            float *p = gb + (int64_t)l * O + o0 + tid;
-            *p = ACCUMULATE ? *p + bsum : bsum;
-        }
+        wait_loads<0>();
+        slot_end();
     }
+}
+
+// A block sums 256 columns of one expert's rows.
+__global__ __launch_bounds__(256) void bias_grad_kernel(const uint16_t *__restrict__ gy,
+                                                        const int32_t *__restrict__ off, int32_t max_rows,
+                                                        int32_t O, bool accumulate, float *__restrict__ gb)
+{
+    const int32_t o = blockIdx.x * 256 + threadIdx.x, l = blockIdx.y;
+    const Rows r = expert_rows(off, l, max_rows);
+    if (o >= O)
+        return;
+    float s = 0.f;
+    for (int64_t i = r.begin; i < r.end; ++i)
+        s += bf16_to_f32(gy[i * O + o]);
+    float *q = gb + (int64_t)l * O + o;
+    *q = accumulate ? *q + s : s;
 }
 
 }  // namespace
@@ -74,18 +94,26 @@ hipError_t launch_expert_wgrad(const uint16_t *grad_y, const uint16_t *x, const 
                                bool accumulate, void *grad_W, float *grad_bias, void *,
                                hipStream_t stream)
 {
-    const int64_t tiles = (int64_t)El * ((O + kBM - 1) / kBM) * ((H + kBN - 1) / kBN);
-    const dim3 grid((unsigned)(tiles < kMaxBlocks ? tiles : kMaxBlocks));
-#define MOE_WGRAD_LAUNCH(F, A)                                                                     \
-    hipLaunchKernelGGL((wgrad_kernel<F, A>), grid, dim3(kThreads), 0, stream, grad_y, x, off, El, \
-                       (int32_t)max_rows, O, H, grad_W, grad_bias)
+    int device = 0, cus = 0;
+    hipError_t err = hipGetDevice(&device);
+    if (err == hipSuccess)
+        err = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
+    if (err != hipSuccess)
+        return err;
+    const int64_t tiles = (int64_t)El * ((O + kTile - 1) / kTile) * ((H + kTile - 1) / kTile);
+    const dim3 grid((unsigned)(tiles < cus ? tiles : cus));
+    const WgradArgs p = {grad_y, x, off, grad_W, El, (int32_t)max_rows, O, H};
     if (accumulate)
-        MOE_WGRAD_LAUNCH(true, true);
+        hipLaunchKernelGGL((wgrad_kernel<true, true>), grid, dim3(kGemmThreads), 0, stream, p);
     else if (fp32)
-        MOE_WGRAD_LAUNCH(true, false);
+        hipLaunchKernelGGL((wgrad_kernel<true, false>), grid, dim3(kGemmThreads), 0, stream, p);
     else
-        MOE_WGRAD_LAUNCH(false, false);
-#undef MOE_WGRAD_LAUNCH
+        hipLaunchKernelGGL((wgrad_kernel<false, false>), grid, dim3(kGemmThreads), 0, stream, p);
+    err = hipGetLastError();
+    if (err != hipSuccess || !grad_bias)
+        return err;
+    hipLaunchKernelGGL(bias_grad_kernel, dim3((unsigned)((O + 255) / 256), (unsigned)El), dim3(256), 0, stream,
+                       grad_y, off, (int32_t)max_rows, O, accumulate, grad_bias);
     return hipGetLastError();
 }
 
