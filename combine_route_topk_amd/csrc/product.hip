@@ -11,18 +11,10 @@
 namespace moe {
 namespace {
 
-__device__ __forceinline__ f32x4 load_bf16x4(const uint16_t *p)
-{
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    return {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
-}
-__device__ __forceinline__ void store_bf16x4(uint16_t *p, f32x4 v)
-{
-    uint2 o;
-    o.x = pack_bf16x2(v[0], v[1]);
-    o.y = pack_bf16x2(v[2], v[3]);
-    *reinterpret_cast<uint2 *>(p) = o;
-}
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ f32x4 widen(u32x2 v) { return {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)}; }
+__device__ __forceinline__ u32x2 narrow(f32x4 v) { return {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; }
 
 struct ProductArgs {
     const uint16_t *a;         // x, or grad_y (GRAD)
@@ -32,50 +24,116 @@ struct ProductArgs {
     int32_t El, max_rows, K, N;  // N: columns before a gate doubles them
 };
 
-// four columns of one row, c a multiple of 4
-template <bool GRAD, bool GATED, int ACT>
-__device__ __forceinline__ void finish(const ProductArgs &p, int32_t l, int64_t row, int32_t c, f32x4 v, f32x4 g)
+// A tile's rows of a [rows][ld] bf16 tensor, read and written four columns at
+// a time through a descriptor that ends with the tile's last row.
+struct TileRows {
+    __amdgpu_buffer_rsrc_t r;
+    uint32_t lane_row;  // byte offset of this lane's row, row (lane & 15) of 16
+    uint32_t ld2;       // bytes of a row
+    __device__ __forceinline__ void init(const uint16_t *p, int64_t row0, int32_t rows, int64_t ld, int lane)
+    {
+        r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p + row0 * ld), 0, (uint32_t)(rows * ld * 2),
+                                              kGemmBufferFlags);
+        ld2 = (uint32_t)ld * 2;
+        lane_row = (uint32_t)(lane & 15) * ld2;
+    }
+    // m: uniform first row of 16, below the tile's rows; col: this lane's byte
+    // offset, kOutside or more where it lies past the width
+    __device__ __forceinline__ f32x4 load(uint32_t m, uint32_t col, uint32_t half = 0) const
+    {
+        return widen(__builtin_bit_cast(
+            u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, lane_row + col, m * ld2 + half, 0)));
+    }
+    __device__ __forceinline__ void store(uint32_t m, uint32_t col, f32x4 v, uint32_t half = 0) const
+    {
+        __builtin_amdgcn_raw_buffer_store_b64(narrow(v), r, lane_row + col, m * ld2 + half, 0);
+    }
+};
+
+// Bias, activation, gate, residual (or the activation's gradient) on the
+// sums, and their one rounding. A group of 16 rows past the tile's last is
+// skipped; the rest is without branches: the descriptors drop rows and
+// columns outside.
+template <bool GRAD, bool GATED, int ACT, class G>
+__device__ __forceinline__ void epilogue(const ProductArgs &p, const G &gemm, const Acc &acc, int32_t l,
+                                         int32_t row0, int32_t rows, int32_t n0)
 {
-    const int64_t N = p.N;
+    constexpr bool PAIR = GATED && !GRAD;
+    constexpr int NC = PAIR ? 2 : 4;  // groups of four columns of a lane
+    const int64_t N = p.N, wide = GATED ? 2 * N : N;
+    const uint32_t N2 = (uint32_t)N * 2;
+    uint32_t col[NC];
+    f32x4 b[NC], bu[NC];
+#pragma unroll
+    for (int q = 0; q < NC; ++q) {
+        const int32_t c = PAIR ? n0 + q * 64 + gemm.wn * 16 + (gemm.lane >> 4) * 4
+                               : n0 + (q >> 1) * 128 + gemm.wn * 32 + (q & 1) * 16 + (gemm.lane >> 4) * 4;
+        col[q] = c < N ? (uint32_t)c * 2 : kOutside;
+        b[q] = bu[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (!GRAD && p.bias && c < N) {
+            b[q] = widen(*reinterpret_cast<const u32x2 *>(p.bias + l * wide + c));
+            if (PAIR)
+                bu[q] = widen(*reinterpret_cast<const u32x2 *>(p.bias + l * wide + N + c));
+        }
+    }
+    TileRows out, aux;
+    out.init(p.out, row0, rows, GRAD ? wide : N, gemm.lane);
     if (GRAD) {
-        if (GATED) {
-            const f32x4 z = load_bf16x4(p.pre_in + row * 2 * N + c), u = load_bf16x4(p.pre_in + row * 2 * N + N + c);
-            f32x4 dz, du;
+        if (p.pre_in)
+            aux.init(p.pre_in, row0, rows, wide, gemm.lane);
+    } else if (p.residual) {
+        aux.init(p.residual, row0, rows, N, gemm.lane);
+    }
+    TileRows pre;
+    if (!GRAD && p.pre_out)
+        pre.init(p.pre_out, row0, rows, wide, gemm.lane);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                dz[i] = v[i] * u[i] * act_grad<ACT>(z[i]);
-                du[i] = v[i] * act<ACT>(z[i]);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int32_t m = h * 128 + gemm.wm * 64 + i * 16;
+            if (m >= rows)
+                continue;
+#pragma unroll
+            for (int q = 0; q < NC; ++q) {
+                f32x4 v = PAIR ? acc[h][q][i][0] : acc[h][q >> 1][i][q & 1];
+                if (GRAD && GATED) {
+                    const f32x4 z = aux.load(m, col[q]), u = aux.load(m, col[q], N2);
+                    f32x4 dz, du;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        dz[e] = v[e] * u[e] * act_grad<ACT>(z[e]);
+                        du[e] = v[e] * act<ACT>(z[e]);
+                    }
+                    out.store(m, col[q], dz);
+                    out.store(m, col[q], du, N2);
+                } else if (GRAD) {
+                    if (p.pre_in) {
+                        const f32x4 z = aux.load(m, col[q]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] *= act_grad<ACT>(z[e]);
+                    }
+                    out.store(m, col[q], v);
+                } else {
+                    v += b[q];
+                    f32x4 g = f32x4{};
+                    if (PAIR)
+                        g = acc[h][q][i][1] + bu[q];
+                    if (p.pre_out) {
+                        pre.store(m, col[q], v);
+                        if (PAIR)
+                            pre.store(m, col[q], g, N2);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = PAIR ? act<ACT>(v[e]) * g[e] : act<ACT>(v[e]);
+                    if (p.residual)
+                        v += aux.load(m, col[q]);
+                    out.store(m, col[q], v);
+                }
             }
-            store_bf16x4(p.out + row * 2 * N + c, dz);
-            store_bf16x4(p.out + row * 2 * N + N + c, du);
-            return;
         }
-        if (p.pre_in) {
-            const f32x4 z = load_bf16x4(p.pre_in + row * N + c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] *= act_grad<ACT>(z[i]);
-        }
-        store_bf16x4(p.out + row * N + c, v);
-        return;
-    }
-    const int64_t wide = GATED ? 2 * N : N;
-    if (p.bias) {
-        v += load_bf16x4(p.bias + l * wide + c);
-        if (GATED)
-            g += load_bf16x4(p.bias + l * wide + N + c);
-    }
-    if (p.pre_out) {
-        store_bf16x4(p.pre_out + row * wide + c, v);
-        if (GATED)
-            store_bf16x4(p.pre_out + row * wide + N + c, g);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        v[i] = GATED ? act<ACT>(v[i]) * g[i] : act<ACT>(v[i]);
-    if (p.residual)
-        v += load_bf16x4(p.residual + row * N + c);
-    store_bf16x4(p.out + row * N + c, v);
 }
 
 template <bool GRAD, bool GATED, int ACT>
@@ -117,29 +175,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_kernel(ProductArgs p)
         Acc acc;
         gemm.start(lds, nk);
         gemm.run(lds, nk, acc);
-#pragma unroll
-        for (int ha = 0; ha < 2; ++ha)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int32_t m = ha * 128 + gemm.wm * 64 + i * 16 + (gemm.lane & 15);
-                if (m >= rows)
-                    continue;
-#pragma unroll
-                for (int hb = 0; hb < 2; ++hb) {
-                    if (PAIR) {
-                        const int32_t c = n0 + hb * 64 + gemm.wn * 16 + (gemm.lane >> 4) * 4;
-                        if (c < p.N)
-                            finish<GRAD, GATED, ACT>(p, l, (int64_t)row0 + m, c, acc[ha][hb][i][0], acc[ha][hb][i][1]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int32_t c = n0 + hb * 128 + gemm.wn * 32 + j * 16 + (gemm.lane >> 4) * 4;
-                            if (c < p.N)
-                                finish<GRAD, GATED, ACT>(p, l, (int64_t)row0 + m, c, acc[ha][hb][i][j], f32x4{});
-                        }
-                    }
-                }
-            }
+        epilogue<GRAD, GATED, ACT>(p, gemm, acc, l, row0, rows, n0);
         wait_loads<0>();
         slot_end();
     }

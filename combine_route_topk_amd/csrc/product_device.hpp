@@ -97,7 +97,13 @@ __device__ __forceinline__ int32_t tile_expert(const int32_t *first, int32_t El,
 // float32, and SiLU's are once |z| > 104.
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+// 2^x and 1 / x by the hardware's instructions, each within a step or two of
+// float32: an activation's value is rounded to bf16 next, 2^16 times coarser.
+// Where exp(-z) overflows the quotient is 0, which misses at most 2^-126.
+__device__ __forceinline__ float sigmoid(float z)
+{
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
+}
 
 constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
@@ -134,7 +140,7 @@ __device__ __forceinline__ float act_grad(float z)
     }
     case kActGelu: {
         const float b = fminf(fmaxf(z, -30.f), 30.f);
-        return 0.5f * erfcf(-b * kSqrtHalf) + b * expf(-0.5f * b * b) * kInvSqrt2Pi;
+        return 0.5f * erfcf(-b * kSqrtHalf) + b * __builtin_amdgcn_exp2f(-0.72134752044448170f * b * b) * kInvSqrt2Pi;
     }
     case kActGeluTanh: {
         const float b = fminf(fmaxf(z, -30.f), 30.f), p = gelu_tanh_cdf(b);
