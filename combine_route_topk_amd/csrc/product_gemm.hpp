@@ -119,11 +119,13 @@ struct Operand {
     }
 };
 
-// Fragment reads. They are written as instructions, each block with its own
-// wait, because the compiler takes every LDS read to depend on every load into
-// LDS in flight and would drain the queue before each; the schedule orders
-// them with barriers and counted waits instead. LDS addresses are byte
-// offsets in 32 bits.
+// Fragment reads. They are written as instructions, because the compiler takes
+// every LDS read to depend on every load into LDS in flight and would drain
+// the queue before each; the schedule orders them with barriers and counted
+// waits instead. A block holds a slot's reads, the wait for the loads that the
+// next phase reads, the barrier that ends the slot, and the wait for the
+// reads themselves, whose latency so passes under the barrier. LDS
+// addresses are byte offsets in 32 bits.
 __device__ __forceinline__ uint32_t lds_offset(const uint8_t *p)
 {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)p;
@@ -147,99 +149,132 @@ __device__ __forceinline__ bf16x8 join(s16x4 lo, s16x4 hi)
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// four fragments of 16 rows each, both halves of a K-tile
+// A: four fragments of 16 rows, B: two of 16 columns, both halves of a K-tile
 struct FragA {
     bf16x8 v[2][4];
 };
-// two fragments of 16 columns each
 struct FragB {
     bf16x8 v[2][2];
 };
 
-template <bool STRIDED>
-struct AddrA {
-    uint32_t a[STRIDED ? 4 : 2];
+#define MOE_READ(d, a, o) "ds_read_b128 %" #d ", %" #a " offset:" #o "\n\t"
+#define MOE_READ_TR(d, a, o) "ds_read_b64_tr_b16 %" #d ", %" #a " offset:" #o "\n\t"
+// destination numbers d.., address numbers a..
+#define MOE_READ_A(d0, d1, d2, d3, d4, d5, d6, d7, a0, a1)                                              \
+    MOE_READ(d0, a0, 0) MOE_READ(d1, a0, 2048) MOE_READ(d2, a0, 4096) MOE_READ(d3, a0, 6144)            \
+    MOE_READ(d4, a1, 0) MOE_READ(d5, a1, 2048) MOE_READ(d6, a1, 4096) MOE_READ(d7, a1, 6144)
+#define MOE_READ_B(d0, d1, d2, d3, a0, a1) \
+    MOE_READ(d0, a0, 0) MOE_READ(d1, a0, 2048) MOE_READ(d2, a1, 0) MOE_READ(d3, a1, 2048)
+#define MOE_READ_TR4(d0, d1, d2, d3, a) \
+    MOE_READ_TR(d0, a, 0) MOE_READ_TR(d1, a, 1024) MOE_READ_TR(d2, a, 8192) MOE_READ_TR(d3, a, 9216)
+#define MOE_BARRIER "s_barrier\n\ts_waitcnt lgkmcnt(0)"
+#define MOE_OUT_A(r)                                                                                    \
+    "=&v"(r.v[0][0]), "=&v"(r.v[0][1]), "=&v"(r.v[0][2]), "=&v"(r.v[0][3]), "=&v"(r.v[1][0]),           \
+        "=&v"(r.v[1][1]), "=&v"(r.v[1][2]), "=&v"(r.v[1][3])
+#define MOE_OUT_B(r) "=&v"(r.v[0][0]), "=&v"(r.v[0][1]), "=&v"(r.v[1][0]), "=&v"(r.v[1][1])
+#define MOE_OUT_TR4(q) "=&v"(q[0]), "=&v"(q[1]), "=&v"(q[2]), "=&v"(q[3])
+
+// the four transposing reads of one fragment: k 0-3, 4-7 of this lane's first
+// eight, then of the eight 32 further
+typedef s16x4 TrFrag[4];
+template <int N, class F>
+__device__ __forceinline__ void from_tr(const TrFrag (&q)[N], F &r)
+{
+#pragma unroll
+    for (int f = 0; f < N; ++f) {
+        r.v[0][f] = join(q[f][0], q[f][1]);
+        r.v[1][f] = join(q[f][2], q[f][3]);
+    }
+}
+
+template <bool STRIDED, int N>
+struct FragAddr {
+    uint32_t a[STRIDED ? N : 2];
     __device__ __forceinline__ void init(int first, int lane)
     {
 #pragma unroll
-        for (int f = 0; f < (STRIDED ? 4 : 2); ++f)
+        for (int f = 0; f < (STRIDED ? N : 2); ++f)
             a[f] = STRIDED ? frag_strided(first, f, lane) : frag_row(first, f, lane);
-    }
-    __device__ __forceinline__ void read(uint32_t half, FragA &r) const
-    {
-        if constexpr (STRIDED) {
-            s16x4 q[2][4][2];
-            asm volatile("ds_read_b64_tr_b16 %0, %16\n\tds_read_b64_tr_b16 %1, %16 offset:1024\n\t"
-                         "ds_read_b64_tr_b16 %2, %17\n\tds_read_b64_tr_b16 %3, %17 offset:1024\n\t"
-                         "ds_read_b64_tr_b16 %4, %18\n\tds_read_b64_tr_b16 %5, %18 offset:1024\n\t"
-                         "ds_read_b64_tr_b16 %6, %19\n\tds_read_b64_tr_b16 %7, %19 offset:1024\n\t"
-                         "ds_read_b64_tr_b16 %8, %16 offset:8192\n\tds_read_b64_tr_b16 %9, %16 offset:9216\n\t"
-                         "ds_read_b64_tr_b16 %10, %17 offset:8192\n\tds_read_b64_tr_b16 %11, %17 offset:9216\n\t"
-                         "ds_read_b64_tr_b16 %12, %18 offset:8192\n\tds_read_b64_tr_b16 %13, %18 offset:9216\n\t"
-                         "ds_read_b64_tr_b16 %14, %19 offset:8192\n\tds_read_b64_tr_b16 %15, %19 offset:9216\n\t"
-                         "s_waitcnt lgkmcnt(0)"
-                         : "=&v"(q[0][0][0]), "=&v"(q[0][0][1]), "=&v"(q[0][1][0]), "=&v"(q[0][1][1]),
-                           "=&v"(q[0][2][0]), "=&v"(q[0][2][1]), "=&v"(q[0][3][0]), "=&v"(q[0][3][1]),
-                           "=&v"(q[1][0][0]), "=&v"(q[1][0][1]), "=&v"(q[1][1][0]), "=&v"(q[1][1][1]),
-                           "=&v"(q[1][2][0]), "=&v"(q[1][2][1]), "=&v"(q[1][3][0]), "=&v"(q[1][3][1])
-                         : "v"(half + a[0]), "v"(half + a[1]), "v"(half + a[2]), "v"(half + a[3])
-                         : "memory");
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int f = 0; f < 4; ++f)
-                    r.v[kk][f] = join(q[kk][f][0], q[kk][f][1]);
-        } else {
-            asm volatile("ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:2048\n\t"
-                         "ds_read_b128 %2, %8 offset:4096\n\tds_read_b128 %3, %8 offset:6144\n\t"
-                         "ds_read_b128 %4, %9\n\tds_read_b128 %5, %9 offset:2048\n\t"
-                         "ds_read_b128 %6, %9 offset:4096\n\tds_read_b128 %7, %9 offset:6144\n\t"
-                         "s_waitcnt lgkmcnt(0)"
-                         : "=&v"(r.v[0][0]), "=&v"(r.v[0][1]), "=&v"(r.v[0][2]), "=&v"(r.v[0][3]),
-                           "=&v"(r.v[1][0]), "=&v"(r.v[1][1]), "=&v"(r.v[1][2]), "=&v"(r.v[1][3])
-                         : "v"(half + a[0]), "v"(half + a[1])
-                         : "memory");
-        }
     }
 };
 
+// Phase 0: B's first half and A's. B's reads are complete at the barrier (A's
+// eight, or sixteen of which the counter sees fifteen, may not be): its half
+// tile is refilled in the next slot. The others are refilled a phase later.
+template <bool ASTR, bool BSTR>
+__device__ __forceinline__ void slot0(const FragAddr<ASTR, 4> &fa, const FragAddr<BSTR, 2> &fb, uint32_t A0,
+                                      uint32_t B0, FragA &a, FragB &b)
+{
+    if constexpr (ASTR) {
+        static_assert(BSTR, "");
+        TrFrag qa[4], qb[2];
+        asm volatile(MOE_READ_TR4(0, 1, 2, 3, 24) MOE_READ_TR4(4, 5, 6, 7, 25)
+                         MOE_READ_TR4(8, 9, 10, 11, 26) MOE_READ_TR4(12, 13, 14, 15, 27)
+                             MOE_READ_TR4(16, 17, 18, 19, 28) MOE_READ_TR4(20, 21, 22, 23, 29)
+                     "s_waitcnt vmcnt(10) lgkmcnt(15)\n\t" MOE_BARRIER
+                     : MOE_OUT_TR4(qb[0]), MOE_OUT_TR4(qb[1]), MOE_OUT_TR4(qa[0]), MOE_OUT_TR4(qa[1]),
+                       MOE_OUT_TR4(qa[2]), MOE_OUT_TR4(qa[3])
+                     : "v"(B0 + fb.a[0]), "v"(B0 + fb.a[1]), "v"(A0 + fa.a[0]), "v"(A0 + fa.a[1]),
+                       "v"(A0 + fa.a[2]), "v"(A0 + fa.a[3])
+                     : "memory");
+        from_tr(qa, a);
+        from_tr(qb, b);
+    } else if constexpr (BSTR) {
+        TrFrag qb[2];
+        asm volatile(MOE_READ_TR4(8, 9, 10, 11, 18) MOE_READ_TR4(12, 13, 14, 15, 19)
+                         MOE_READ_A(0, 1, 2, 3, 4, 5, 6, 7, 16, 17)
+                     "s_waitcnt vmcnt(10) lgkmcnt(8)\n\t" MOE_BARRIER
+                     : MOE_OUT_A(a), MOE_OUT_TR4(qb[0]), MOE_OUT_TR4(qb[1])
+                     : "v"(A0 + fa.a[0]), "v"(A0 + fa.a[1]), "v"(B0 + fb.a[0]), "v"(B0 + fb.a[1])
+                     : "memory");
+        from_tr(qb, b);
+    } else {
+        asm volatile(MOE_READ_B(8, 9, 10, 11, 14, 15) MOE_READ_A(0, 1, 2, 3, 4, 5, 6, 7, 12, 13)
+                     "s_waitcnt vmcnt(10) lgkmcnt(8)\n\t" MOE_BARRIER
+                     : MOE_OUT_A(a), MOE_OUT_B(b)
+                     : "v"(A0 + fa.a[0]), "v"(A0 + fa.a[1]), "v"(B0 + fb.a[0]), "v"(B0 + fb.a[1])
+                     : "memory");
+    }
+}
+
+// Phase 1: B's second half.
 template <bool STRIDED>
-struct AddrB {
-    uint32_t a[2];
-    __device__ __forceinline__ void init(int first, int lane)
-    {
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-            a[f] = STRIDED ? frag_strided(first, f, lane) : frag_row(first, f, lane);
+__device__ __forceinline__ void slot1(const FragAddr<STRIDED, 2> &fb, uint32_t B1, FragB &b)
+{
+    if constexpr (STRIDED) {
+        TrFrag q[2];
+        asm volatile(MOE_READ_TR4(0, 1, 2, 3, 8) MOE_READ_TR4(4, 5, 6, 7, 9) "s_waitcnt vmcnt(10)\n\t" MOE_BARRIER
+                     : MOE_OUT_TR4(q[0]), MOE_OUT_TR4(q[1])
+                     : "v"(B1 + fb.a[0]), "v"(B1 + fb.a[1])
+                     : "memory");
+        from_tr(q, b);
+    } else {
+        asm volatile(MOE_READ_B(0, 1, 2, 3, 4, 5) "s_waitcnt vmcnt(10)\n\t" MOE_BARRIER
+                     : MOE_OUT_B(b)
+                     : "v"(B1 + fb.a[0]), "v"(B1 + fb.a[1])
+                     : "memory");
     }
-    __device__ __forceinline__ void read(uint32_t half, FragB &r) const
-    {
-        if constexpr (STRIDED) {
-            s16x4 q[2][2][2];
-            asm volatile("ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %8 offset:1024\n\t"
-                         "ds_read_b64_tr_b16 %2, %9\n\tds_read_b64_tr_b16 %3, %9 offset:1024\n\t"
-                         "ds_read_b64_tr_b16 %4, %8 offset:8192\n\tds_read_b64_tr_b16 %5, %8 offset:9216\n\t"
-                         "ds_read_b64_tr_b16 %6, %9 offset:8192\n\tds_read_b64_tr_b16 %7, %9 offset:9216\n\t"
-                         "s_waitcnt lgkmcnt(0)"
-                         : "=&v"(q[0][0][0]), "=&v"(q[0][0][1]), "=&v"(q[0][1][0]), "=&v"(q[0][1][1]),
-                           "=&v"(q[1][0][0]), "=&v"(q[1][0][1]), "=&v"(q[1][1][0]), "=&v"(q[1][1][1])
-                         : "v"(half + a[0]), "v"(half + a[1])
-                         : "memory");
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-                    r.v[kk][f] = join(q[kk][f][0], q[kk][f][1]);
-        } else {
-            asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:2048\n\t"
-                         "ds_read_b128 %2, %5\n\tds_read_b128 %3, %5 offset:2048\n\t"
-                         "s_waitcnt lgkmcnt(0)"
-                         : "=&v"(r.v[0][0]), "=&v"(r.v[0][1]), "=&v"(r.v[1][0]), "=&v"(r.v[1][1])
-                         : "v"(half + a[0]), "v"(half + a[1])
-                         : "memory");
-        }
+}
+
+// Phase 2: A's second half.
+template <bool STRIDED>
+__device__ __forceinline__ void slot2(const FragAddr<STRIDED, 4> &fa, uint32_t A1, FragA &a)
+{
+    if constexpr (STRIDED) {
+        TrFrag q[4];
+        asm volatile(MOE_READ_TR4(0, 1, 2, 3, 16) MOE_READ_TR4(4, 5, 6, 7, 17) MOE_READ_TR4(8, 9, 10, 11, 18)
+                         MOE_READ_TR4(12, 13, 14, 15, 19) MOE_BARRIER
+                     : MOE_OUT_TR4(q[0]), MOE_OUT_TR4(q[1]), MOE_OUT_TR4(q[2]), MOE_OUT_TR4(q[3])
+                     : "v"(A1 + fa.a[0]), "v"(A1 + fa.a[1]), "v"(A1 + fa.a[2]), "v"(A1 + fa.a[3])
+                     : "memory");
+        from_tr(q, a);
+    } else {
+        asm volatile(MOE_READ_A(0, 1, 2, 3, 4, 5, 6, 7, 8, 9) MOE_BARRIER
+                     : MOE_OUT_A(a)
+                     : "v"(A1 + fa.a[0]), "v"(A1 + fa.a[1])
+                     : "memory");
     }
-};
+}
 
 // wait until at most N of this wave's vector-memory operations are outstanding
 template <int N>
@@ -264,8 +299,8 @@ template <bool ASTR, bool BSTR>
 struct Gemm {
     Operand<ASTR> A;
     Operand<BSTR> B;
-    AddrA<ASTR> fa;
-    AddrB<BSTR> fb;
+    FragAddr<ASTR, 4> fa;
+    FragAddr<BSTR, 2> fb;
     int wave, lane, wm, wn;
 
     __device__ __forceinline__ void init_lane()
@@ -293,6 +328,7 @@ struct Gemm {
 
     __device__ __forceinline__ static void mfmas(const FragA &a, const FragB &b, f32x4 (&c)[4][2])
     {
+        __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
@@ -305,35 +341,25 @@ struct Gemm {
     }
 
     // K-tile t, which lies in stage `cur`. A slot between two barriers holds
-    // either reads and load starts or MFMAs; each half tile is read by the last
-    // wave, and waited for, a barrier before its refill is started.
+    // either reads and load starts or MFMAs; each half tile's refill is started
+    // a barrier or more after every wave's reads of it are complete.
     __device__ __forceinline__ void ktile(uint8_t *cur, uint8_t *other, int t, int nk, Acc &acc) const
     {
         const uint32_t at = lds_offset(cur);
         FragA a;
         FragB bl, bh;
-        // phase 0
         A.load(other + kHalfBytes, 1, t + 1, nk, wave);
-        fb.read(at + 2 * kHalfBytes, bl);
-        fa.read(at, a);
-        wait_loads<10>();
-        slot_end();
+        slot0<ASTR, BSTR>(fa, fb, at, at + 2 * kHalfBytes, a, bl);
         mfmas(a, bl, acc[0][0]);
         slot_end();
-        // phase 1
         B.load(cur + 2 * kHalfBytes, 0, t + 2, nk, wave);
-        fb.read(at + 3 * kHalfBytes, bh);
-        wait_loads<10>();
-        slot_end();
+        slot1<BSTR>(fb, at + 3 * kHalfBytes, bh);
         mfmas(a, bh, acc[0][1]);
         slot_end();
-        // phase 2
         A.load(cur, 0, t + 2, nk, wave);
-        fa.read(at + kHalfBytes, a);
-        slot_end();
+        slot2<ASTR>(fa, at + kHalfBytes, a);
         mfmas(a, bh, acc[1][1]);
         slot_end();
-        // phase 3
         B.load(cur + 3 * kHalfBytes, 1, t + 2, nk, wave);
         wait_loads<10>();
         slot_end();
