@@ -167,7 +167,7 @@ struct FragB {
     MOE_READ(d0, a0, 0) MOE_READ(d1, a0, 2048) MOE_READ(d2, a1, 0) MOE_READ(d3, a1, 2048)
 #define MOE_READ_TR4(d0, d1, d2, d3, a) \
     MOE_READ_TR(d0, a, 0) MOE_READ_TR(d1, a, 1024) MOE_READ_TR(d2, a, 8192) MOE_READ_TR(d3, a, 9216)
-#define MOE_BARRIER "s_barrier\n\ts_waitcnt lgkmcnt(0)"
+#define MOE_SLOT_END "s_waitcnt vmcnt(10)\n\ts_barrier\n\ts_waitcnt lgkmcnt(0)"
 #define MOE_OUT_A(r)                                                                                    \
     "=&v"(r.v[0][0]), "=&v"(r.v[0][1]), "=&v"(r.v[0][2]), "=&v"(r.v[0][3]), "=&v"(r.v[1][0]),           \
         "=&v"(r.v[1][1]), "=&v"(r.v[1][2]), "=&v"(r.v[1][3])
@@ -198,80 +198,39 @@ struct FragAddr {
     }
 };
 
-// Phase 0: B's first half and A's. B's reads are complete at the barrier (A's
-// eight, or sixteen of which the counter sees fifteen, may not be): its half
-// tile is refilled in the next slot. The others are refilled a phase later.
-template <bool ASTR, bool BSTR>
-__device__ __forceinline__ void slot0(const FragAddr<ASTR, 4> &fa, const FragAddr<BSTR, 2> &fb, uint32_t A0,
-                                      uint32_t B0, FragA &a, FragB &b)
-{
-    if constexpr (ASTR) {
-        static_assert(BSTR, "");
-        TrFrag qa[4], qb[2];
-        asm volatile(MOE_READ_TR4(0, 1, 2, 3, 24) MOE_READ_TR4(4, 5, 6, 7, 25)
-                         MOE_READ_TR4(8, 9, 10, 11, 26) MOE_READ_TR4(12, 13, 14, 15, 27)
-                             MOE_READ_TR4(16, 17, 18, 19, 28) MOE_READ_TR4(20, 21, 22, 23, 29)
-                     "s_waitcnt vmcnt(10) lgkmcnt(15)\n\t" MOE_BARRIER
-                     : MOE_OUT_TR4(qb[0]), MOE_OUT_TR4(qb[1]), MOE_OUT_TR4(qa[0]), MOE_OUT_TR4(qa[1]),
-                       MOE_OUT_TR4(qa[2]), MOE_OUT_TR4(qa[3])
-                     : "v"(B0 + fb.a[0]), "v"(B0 + fb.a[1]), "v"(A0 + fa.a[0]), "v"(A0 + fa.a[1]),
-                       "v"(A0 + fa.a[2]), "v"(A0 + fa.a[3])
-                     : "memory");
-        from_tr(qa, a);
-        from_tr(qb, b);
-    } else if constexpr (BSTR) {
-        TrFrag qb[2];
-        asm volatile(MOE_READ_TR4(8, 9, 10, 11, 18) MOE_READ_TR4(12, 13, 14, 15, 19)
-                         MOE_READ_A(0, 1, 2, 3, 4, 5, 6, 7, 16, 17)
-                     "s_waitcnt vmcnt(10) lgkmcnt(8)\n\t" MOE_BARRIER
-                     : MOE_OUT_A(a), MOE_OUT_TR4(qb[0]), MOE_OUT_TR4(qb[1])
-                     : "v"(A0 + fa.a[0]), "v"(A0 + fa.a[1]), "v"(B0 + fb.a[0]), "v"(B0 + fb.a[1])
-                     : "memory");
-        from_tr(qb, b);
-    } else {
-        asm volatile(MOE_READ_B(8, 9, 10, 11, 14, 15) MOE_READ_A(0, 1, 2, 3, 4, 5, 6, 7, 12, 13)
-                     "s_waitcnt vmcnt(10) lgkmcnt(8)\n\t" MOE_BARRIER
-                     : MOE_OUT_A(a), MOE_OUT_B(b)
-                     : "v"(A0 + fa.a[0]), "v"(A0 + fa.a[1]), "v"(B0 + fb.a[0]), "v"(B0 + fb.a[1])
-                     : "memory");
-    }
-}
-
-// Phase 1: B's second half.
+// The slot that reads a half of B, and the one that reads a half of A.
 template <bool STRIDED>
-__device__ __forceinline__ void slot1(const FragAddr<STRIDED, 2> &fb, uint32_t B1, FragB &b)
+__device__ __forceinline__ void slot_b(const FragAddr<STRIDED, 2> &fb, uint32_t half, FragB &b)
 {
     if constexpr (STRIDED) {
         TrFrag q[2];
-        asm volatile(MOE_READ_TR4(0, 1, 2, 3, 8) MOE_READ_TR4(4, 5, 6, 7, 9) "s_waitcnt vmcnt(10)\n\t" MOE_BARRIER
+        asm volatile(MOE_READ_TR4(0, 1, 2, 3, 8) MOE_READ_TR4(4, 5, 6, 7, 9) MOE_SLOT_END
                      : MOE_OUT_TR4(q[0]), MOE_OUT_TR4(q[1])
-                     : "v"(B1 + fb.a[0]), "v"(B1 + fb.a[1])
+                     : "v"(half + fb.a[0]), "v"(half + fb.a[1])
                      : "memory");
         from_tr(q, b);
     } else {
-        asm volatile(MOE_READ_B(0, 1, 2, 3, 4, 5) "s_waitcnt vmcnt(10)\n\t" MOE_BARRIER
+        asm volatile(MOE_READ_B(0, 1, 2, 3, 4, 5) MOE_SLOT_END
                      : MOE_OUT_B(b)
-                     : "v"(B1 + fb.a[0]), "v"(B1 + fb.a[1])
+                     : "v"(half + fb.a[0]), "v"(half + fb.a[1])
                      : "memory");
     }
 }
-
-// Phase 2: A's second half.
 template <bool STRIDED>
-__device__ __forceinline__ void slot2(const FragAddr<STRIDED, 4> &fa, uint32_t A1, FragA &a)
+__device__ __forceinline__ void slot_a(const FragAddr<STRIDED, 4> &fa, uint32_t half, FragA &a)
 {
     if constexpr (STRIDED) {
         TrFrag q[4];
         asm volatile(MOE_READ_TR4(0, 1, 2, 3, 16) MOE_READ_TR4(4, 5, 6, 7, 17) MOE_READ_TR4(8, 9, 10, 11, 18)
-                         MOE_READ_TR4(12, 13, 14, 15, 19) MOE_BARRIER
+                         MOE_READ_TR4(12, 13, 14, 15, 19) MOE_SLOT_END
                      : MOE_OUT_TR4(q[0]), MOE_OUT_TR4(q[1]), MOE_OUT_TR4(q[2]), MOE_OUT_TR4(q[3])
-                     : "v"(A1 + fa.a[0]), "v"(A1 + fa.a[1]), "v"(A1 + fa.a[2]), "v"(A1 + fa.a[3])
+                     : "v"(half + fa.a[0]), "v"(half + fa.a[1]), "v"(half + fa.a[2]), "v"(half + fa.a[3])
                      : "memory");
         from_tr(q, a);
     } else {
-        asm volatile(MOE_READ_A(0, 1, 2, 3, 4, 5, 6, 7, 8, 9) MOE_BARRIER
+        asm volatile(MOE_READ_A(0, 1, 2, 3, 4, 5, 6, 7, 8, 9) MOE_SLOT_END
                      : MOE_OUT_A(a)
-                     : "v"(A1 + fa.a[0]), "v"(A1 + fa.a[1])
+                     : "v"(half + fa.a[0]), "v"(half + fa.a[1])
                      : "memory");
     }
 }
@@ -340,30 +299,31 @@ struct Gemm {
         __builtin_amdgcn_s_setprio(0);
     }
 
-    // K-tile t, which lies in stage `cur`. A slot between two barriers holds
-    // either reads and load starts or MFMAs; each half tile's refill is started
-    // a barrier or more after every wave's reads of it are complete.
-    __device__ __forceinline__ void ktile(uint8_t *cur, uint8_t *other, int t, int nk, Acc &acc) const
+    // K-tile t, which lies in stage `cur`; b0 holds its first half of B, and
+    // next receives the next K-tile's. A slot between two barriers holds either
+    // reads and load starts or MFMAs, and the refill of a half tile starts a
+    // barrier or more after every wave's reads of it are complete.
+    __device__ __forceinline__ void ktile(uint8_t *cur, uint8_t *other, int t, int nk, const FragB &b0, FragB &next,
+                                          Acc &acc) const
     {
-        const uint32_t at = lds_offset(cur);
+        const uint32_t at = lds_offset(cur), then = lds_offset(other);
         FragA a;
-        FragB bl, bh;
+        FragB b1;
         A.load(other + kHalfBytes, 1, t + 1, nk, wave);
-        slot0<ASTR, BSTR>(fa, fb, at, at + 2 * kHalfBytes, a, bl);
-        mfmas(a, bl, acc[0][0]);
+        slot_a<ASTR>(fa, at, a);
+        mfmas(a, b0, acc[0][0]);
         slot_end();
         B.load(cur + 2 * kHalfBytes, 0, t + 2, nk, wave);
-        slot1<BSTR>(fb, at + 3 * kHalfBytes, bh);
-        mfmas(a, bh, acc[0][1]);
+        slot_b<BSTR>(fb, at + 3 * kHalfBytes, b1);
+        mfmas(a, b1, acc[0][1]);
         slot_end();
         A.load(cur, 0, t + 2, nk, wave);
-        slot2<ASTR>(fa, at + kHalfBytes, a);
-        mfmas(a, bh, acc[1][1]);
+        slot_a<ASTR>(fa, at + kHalfBytes, a);
+        mfmas(a, b1, acc[1][1]);
         slot_end();
         B.load(cur + 3 * kHalfBytes, 1, t + 2, nk, wave);
-        wait_loads<10>();
-        slot_end();
-        mfmas(a, bl, acc[1][0]);
+        slot_b<BSTR>(fb, then + 2 * kHalfBytes, next);
+        mfmas(a, b0, acc[1][0]);
         slot_end();
     }
 
@@ -379,15 +339,17 @@ struct Gemm {
         uint8_t *s0 = lds, *s1 = lds + kStageBytes;
         wait_loads<10>();
         slot_end();
+        FragB b0, b1;
+        slot_b<BSTR>(fb, lds_offset(s0 + 2 * kHalfBytes), b0);
         if (wm)  // the second group of waves starts half a phase later
             slot_end();
         int t = 0;
         for (; t + 1 < nk; t += 2) {
-            ktile(s0, s1, t, nk, acc);
-            ktile(s1, s0, t + 1, nk, acc);
+            ktile(s0, s1, t, nk, b0, b1, acc);
+            ktile(s1, s0, t + 1, nk, b1, b0, acc);
         }
         if (t < nk)
-            ktile(s0, s1, t, nk, acc);
+            ktile(s0, s1, t, nk, b0, b1, acc);
         if (!wm)
             slot_end();
     }
