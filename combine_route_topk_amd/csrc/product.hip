@@ -11,43 +11,12 @@
 namespace moe {
 namespace {
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ f32x4 widen(u32x2 v) { return {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)}; }
-__device__ __forceinline__ u32x2 narrow(f32x4 v) { return {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; }
-
 struct ProductArgs {
     const uint16_t *a;         // x, or grad_y (GRAD)
     const int32_t *off;
     const uint16_t *W, *bias, *residual, *pre_in;
     uint16_t *pre_out, *out;
     int32_t El, max_rows, K, N;  // N: columns before a gate doubles them
-};
-
-// A tile's rows of a [rows][ld] bf16 tensor, read and written four columns at
-// a time through a descriptor that ends with the tile's last row.
-struct TileRows {
-    __amdgpu_buffer_rsrc_t r;
-    uint32_t lane_row;  // byte offset of this lane's row, row (lane & 15) of 16
-    uint32_t ld2;       // bytes of a row
-    __device__ __forceinline__ void init(const uint16_t *p, int64_t row0, int32_t rows, int64_t ld, int lane)
-    {
-        r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p + row0 * ld), 0, (uint32_t)(rows * ld * 2),
-                                              kGemmBufferFlags);
-        ld2 = (uint32_t)ld * 2;
-        lane_row = (uint32_t)(lane & 15) * ld2;
-    }
-    // m: uniform first row of 16, below the tile's rows; col: this lane's byte
-    // offset, kOutside or more where it lies past the width
-    __device__ __forceinline__ f32x4 load(uint32_t m, uint32_t col, uint32_t half = 0) const
-    {
-        return widen(__builtin_bit_cast(
-            u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, lane_row + col, m * ld2 + half, 0)));
-    }
-    __device__ __forceinline__ void store(uint32_t m, uint32_t col, f32x4 v, uint32_t half = 0) const
-    {
-        __builtin_amdgcn_raw_buffer_store_b64(narrow(v), r, lane_row + col, m * ld2 + half, 0);
-    }
 };
 
 // Bias, activation, gate, residual (or the activation's gradient) on the
@@ -59,21 +28,25 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, const G &gemm, co
                                          int32_t row0, int32_t rows, int32_t n0)
 {
     constexpr bool PAIR = GATED && !GRAD;
-    constexpr int NC = PAIR ? 2 : 4;  // groups of four columns of a lane
+    constexpr int NP = PAIR ? 1 : 2;  // pairs of a lane's groups of four columns
     const int64_t N = p.N, wide = GATED ? 2 * N : N;
     const uint32_t N2 = (uint32_t)N * 2;
-    uint32_t col[NC];
-    f32x4 b[NC], bu[NC];
+    uint32_t col[NP];
+    f32x4 b[NP][2], bu[NP][2];
 #pragma unroll
-    for (int q = 0; q < NC; ++q) {
-        const int32_t c = PAIR ? n0 + q * 64 + gemm.wn * 16 + (gemm.lane >> 4) * 4
-                               : n0 + (q >> 1) * 128 + gemm.wn * 32 + (q & 1) * 16 + (gemm.lane >> 4) * 4;
-        col[q] = c < N ? (uint32_t)c * 2 : kOutside;
-        b[q] = bu[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (!GRAD && p.bias && c < N) {
-            b[q] = widen(*reinterpret_cast<const u32x2 *>(p.bias + l * wide + c));
-            if (PAIR)
-                bu[q] = widen(*reinterpret_cast<const u32x2 *>(p.bias + l * wide + N + c));
+    for (int q = 0; q < NP; ++q) {
+        const int32_t c0 = n0 + (PAIR ? gemm.wn * 32 : gemm.column(q));
+        const int32_t c8 = c0 + (gemm.lane >> 4) * 8;
+        col[q] = c8 < N ? (uint32_t)c8 * 2 : kOutside;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int32_t c4 = c0 + j * 16 + (gemm.lane >> 4) * 4;
+            b[q][j] = bu[q][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (!GRAD && p.bias && c4 < N) {
+                b[q][j] = widen(*reinterpret_cast<const u32x2 *>(p.bias + l * wide + c4));
+                if (PAIR)
+                    bu[q][j] = widen(*reinterpret_cast<const u32x2 *>(p.bias + l * wide + N + c4));
+            }
         }
     }
     TileRows out, aux;
@@ -95,41 +68,55 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, const G &gemm, co
             if (m >= rows)
                 continue;
 #pragma unroll
-            for (int q = 0; q < NC; ++q) {
-                f32x4 v = PAIR ? acc[h][q][i][0] : acc[h][q >> 1][i][q & 1];
-                if (GRAD && GATED) {
-                    const f32x4 z = aux.load(m, col[q]), u = aux.load(m, col[q], N2);
-                    f32x4 dz, du;
+            for (int q = 0; q < NP; ++q) {
+                f32x4 v[2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        dz[e] = v[e] * u[e] * act_grad<ACT>(z[e]);
-                        du[e] = v[e] * act<ACT>(z[e]);
-                    }
+                for (int j = 0; j < 2; ++j)
+                    v[j] = PAIR ? acc[h][j][i][0] : acc[h][q][i][j];
+                if (GRAD && GATED) {
+                    f32x4 z[2], u[2], dz[2], du[2];
+                    aux.load(m, col[q], z);
+                    aux.load(m, col[q], u, N2);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            dz[j][e] = v[j][e] * u[j][e] * act_grad<ACT>(z[j][e]);
+                            du[j][e] = v[j][e] * act<ACT>(z[j][e]);
+                        }
                     out.store(m, col[q], dz);
                     out.store(m, col[q], du, N2);
                 } else if (GRAD) {
                     if (p.pre_in) {
-                        const f32x4 z = aux.load(m, col[q]);
+                        f32x4 z[2];
+                        aux.load(m, col[q], z);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] *= act_grad<ACT>(z[e]);
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                v[j][e] *= act_grad<ACT>(z[j][e]);
                     }
                     out.store(m, col[q], v);
                 } else {
-                    v += b[q];
-                    f32x4 g = f32x4{};
-                    if (PAIR)
-                        g = acc[h][q][i][1] + bu[q];
+                    f32x4 g[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        v[j] += b[q][j];
+                        g[j] = PAIR ? acc[h][j][i][1] + bu[q][j] : f32x4{};
+                    }
                     if (p.pre_out) {
                         pre.store(m, col[q], v);
                         if (PAIR)
                             pre.store(m, col[q], g, N2);
                     }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = PAIR ? act<ACT>(v[e]) * g[e] : act<ACT>(v[e]);
+                    f32x4 r[2] = {};
                     if (p.residual)
-                        v += aux.load(m, col[q]);
+                        aux.load(m, col[q], r);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[j][e] = (PAIR ? act<ACT>(v[j][e]) * g[j][e] : act<ACT>(v[j][e])) + r[j][e];
                     out.store(m, col[q], v);
                 }
             }
@@ -167,10 +154,11 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_kernel(ProductArgs p)
         } else if constexpr (GATED) {
             // rows of a half: for each wave's 32 columns, 16 gate then 16 up
             const bool up = (gemm.wave >> 1) & 1;
-            gemm.B.init(Wl + ((up ? (int64_t)p.N : 0) + n0) * p.K, p.N - n0, p.K, gemm.wave, gemm.lane, 64,
-                        [](int j) { return (j >> 2) * 16 + (j & 1) * 8; });
+            gemm.B.init(Wl + ((up ? (int64_t)p.N : 0) + n0) * p.K, p.N - n0, p.K, gemm.wave, gemm.lane, 16,
+                        [](int j) { return (j >> 2) * 32 + (j & 1) * 8; });
         } else {
-            gemm.B.init(Wl + (int64_t)n0 * p.K, p.N - n0, p.K, gemm.wave, gemm.lane, 128, [](int j) { return j * 8; });
+            gemm.B.init(Wl + (int64_t)n0 * p.K, p.N - n0, p.K, gemm.wave, gemm.lane, 32,
+                        [](int j) { return (j >> 2) * 64 + (j & 3) * 8; });
         }
         Acc acc;
         gemm.start(lds, nk);

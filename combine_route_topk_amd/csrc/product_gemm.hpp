@@ -55,8 +55,7 @@ struct Operand {
     uint32_t tail;        // kOutside where this lane's piece lies past K in the last K-tile
 
     // K-contiguous: `rows` valid rows of K elements from p. half_rows: rows
-    // between the halves (128, or 64 of a gated W whose halves hold 64 gate
-    // and 64 up columns); row_of: row of load index j within a half.
+    // between the halves; row_of: first of the eight rows of load j of a half.
     template <class RowOf>
     __device__ __forceinline__ void init(const uint16_t *p, int64_t rows, int32_t K, int wave, int lane,
                                          int half_rows, RowOf row_of)
@@ -84,12 +83,12 @@ struct Operand {
         const int kr = lane >> 4, swz = (kr & 3) | (((wave >> 1) & 1) << 2);
         const int c = (lane & 15) ^ (2 * swz);  // piece at LDS position lane % 16
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+            const int n = h * 128 + c * 8;  // column of piece c
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                off[h][i] = h * 128 + c * 8 >= width
-                                ? kOutside
-                                : (uint32_t)((i * 8 + wave) * 4 + kr) * (uint32_t)ld * 2u + h * 256 + c * 16;
+                off[h][i] = n >= width ? kOutside : (uint32_t)((i * 8 + wave) * 4 + kr) * (uint32_t)ld * 2u + n * 2;
+        }
         tail = 0;
     }
 
@@ -250,8 +249,15 @@ __device__ __forceinline__ void slot_end()
 }
 
 // acc[hA][hB][fa][fb]: lane L holds row hA * 128 + wm * 64 + fa * 16 + L % 16
-// and columns hB * 128 + wn * 32 + fb * 16 + (L / 16) * 4 + 0..3 (of the tile
-// as it lies in LDS).
+// and four columns, which lie in LDS as rows (K-strided: columns) wn * 32 +
+// fb * 16 + (L / 16) * 4 + 0..3 of B's half tile hB. K-contiguous, that half
+// holds columns [hB * 32, hB * 32 + 32) of each 64 of the tile (gated: 16 gate
+// and 16 up columns [hB * 16, hB * 16 + 16) of each 32), so that a wave's
+// columns are consecutive: rows of 128 bytes to write, which took 1.63 ms
+// against 1.80 for halves of 128 columns (327680 x 2048 by 2 x 768, gated).
+// K-strided, it holds columns [hB * 128, hB * 128 + 128): splitting its
+// 256-byte pieces into 64 bytes took 608 against 573 us (32768 x 4096 by
+// 2048).
 typedef f32x4 Acc[2][2][4][2];
 
 template <bool ASTR, bool BSTR>
@@ -271,6 +277,9 @@ struct Gemm {
         fa.init(wm * 64, lane);
         fb.init(wn * 32, lane);
     }
+
+    // first of the 32 columns that acc[.][hB] holds for this wave
+    __device__ __forceinline__ int column(int hB) const { return BSTR ? hB * 128 + wn * 32 : wn * 64 + hB * 32; }
 
     // the loads that run ahead of the first phase, in the order they are waited for
     __device__ __forceinline__ void start(uint8_t *lds, int nk) const
@@ -352,6 +361,78 @@ struct Gemm {
             ktile(s0, s1, t, nk, b0, b1, acc);
         if (!wm)
             slot_end();
+    }
+};
+
+// Two groups of four bf16 columns, 16 columns apart, of a row that lies across
+// lanes L, L + 16, L + 32, L + 48 -> eight consecutive columns in each of
+// those lanes, (L / 16) * 8 + 0..7 of 32; and back. One 16-byte access per
+// lane then covers 64 consecutive bytes of 16 rows.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b)
+{
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b)
+{
+    const u32x2 r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ u32x4 to_rows(u32x2 a, u32x2 b)
+{
+    uint32_t a0 = a[0], a1 = a[1], b0 = b[0], b1 = b[1];
+    swap32(a0, b0);
+    swap32(a1, b1);
+    swap16(a0, b0);
+    swap16(a1, b1);
+    return u32x4{a0, a1, b0, b1};
+}
+__device__ __forceinline__ void from_rows(u32x4 v, u32x2 &a, u32x2 &b)
+{
+    uint32_t a0 = v[0], a1 = v[1], b0 = v[2], b1 = v[3];
+    swap16(a0, b0);
+    swap16(a1, b1);
+    swap32(a0, b0);
+    swap32(a1, b1);
+    a = u32x2{a0, a1};
+    b = u32x2{b0, b1};
+}
+__device__ __forceinline__ f32x4 widen(u32x2 v) { return {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)}; }
+__device__ __forceinline__ u32x2 narrow(f32x4 v) { return {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; }
+
+// A tile's rows of a [rows][ld] bf16 tensor, through a descriptor that ends
+// with the tile's last row: pairs of column groups as above, this lane's eight
+// consecutive columns at byte offset col (kOutside or more past the width) of
+// row m + lane % 16, m uniform and below the tile's rows. The stores carry no
+// scalar offset: a 16-byte store with one, followed at once by an instruction
+// that writes its last data register, stored the new value in some lanes on
+// gfx950, and the compiler keeps the two apart only where there is none.
+struct TileRows {
+    __amdgpu_buffer_rsrc_t r;
+    uint32_t lane_row, ld2;
+    __device__ __forceinline__ void init(const uint16_t *p, int64_t row0, int32_t rows, int64_t ld, int lane)
+    {
+        r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p + row0 * ld), 0, (uint32_t)(rows * ld * 2),
+                                              kGemmBufferFlags);
+        ld2 = (uint32_t)ld * 2;
+        lane_row = (uint32_t)(lane & 15) * ld2;
+    }
+    __device__ __forceinline__ void load(uint32_t m, uint32_t col, f32x4 (&v)[2], uint32_t half = 0) const
+    {
+        u32x2 a, b;
+        from_rows(__builtin_bit_cast(
+                      u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_row + col, m * ld2 + half, 0)),
+                  a, b);
+        v[0] = widen(a);
+        v[1] = widen(b);
+    }
+    __device__ __forceinline__ void store(uint32_t m, uint32_t col, const f32x4 (&v)[2], uint32_t half = 0) const
+    {
+        __builtin_amdgcn_raw_buffer_store_b128(to_rows(narrow(v[0]), narrow(v[1])), r,
+                                               lane_row + col + (m * ld2 + half), 0, 0);
     }
 };
 

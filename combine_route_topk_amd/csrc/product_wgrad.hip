@@ -40,29 +40,27 @@ __global__ __launch_bounds__(kGemmThreads, 2) void wgrad_kernel(WgradArgs p)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int32_t o = o0 + ha * 128 + gemm.wm * 64 + i * 16 + (gemm.lane & 15);
-                if (o >= p.O)
-                    continue;
 #pragma unroll
-                for (int hb = 0; hb < 2; ++hb)
+                for (int hb = 0; hb < 2; ++hb) {
+                    const int64_t at = ((int64_t)l * p.O + o) * p.H + h0 + gemm.column(hb);
+                    const int32_t left = p.H - h0 - gemm.column(hb), c4 = (gemm.lane >> 4) * 4;
+                    if (FP32) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int32_t h = h0 + hb * 128 + gemm.wn * 32 + j * 16 + (gemm.lane >> 4) * 4;
-                        if (h >= p.H)
-                            continue;
-                        const int64_t at = ((int64_t)l * p.O + o) * p.H + h;
-                        f32x4 v = acc[ha][hb][i][j];
-                        if (FP32) {
-                            f32x4 *q = reinterpret_cast<f32x4 *>(static_cast<float *>(p.gW) + at);
+                        for (int j = 0; j < 2; ++j) {
+                            if (o >= p.O || j * 16 + c4 >= left)
+                                continue;
+                            f32x4 v = acc[ha][hb][i][j];
+                            f32x4 *q = reinterpret_cast<f32x4 *>(static_cast<float *>(p.gW) + at + j * 16 + c4);
                             if (ACCUMULATE)
                                 v += *q;
                             *q = v;
-                        } else {
-                            uint2 b;
-                            b.x = pack_bf16x2(v[0], v[1]);
-                            b.y = pack_bf16x2(v[2], v[3]);
-                            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.gW) + at) = b;
                         }
+                    } else {
+                        const u32x4 v = to_rows(narrow(acc[ha][hb][i][0]), narrow(acc[ha][hb][i][1]));
+                        if (o < p.O && c4 * 2 < left)
+                            *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.gW) + at + c4 * 2) = v;
                     }
+                }
             }
         wait_loads<0>();
         slot_end();
