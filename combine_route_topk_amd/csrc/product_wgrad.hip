@@ -1,95 +1,267 @@
 // product_wgrad.hip -- the gradients of the experts' weights and biases:
 // grad_W[l] = grad_y[rows of l]^T x[rows of l], summed over the rows in
 // float32. Both operands are K-strided (K is the rows); product_gemm.hpp has
-// the K loop. grad_bias is summed by a kernel of its own.
+// the K loop.
+//
+// Split. A tile is 256 x 256 of one expert's grad_W. With few tiles for the
+// CUs, or a last round that would leave many idle, each expert's rows are cut
+// into S pieces, whose float32 sums go to the workspace and are added in
+// ascending order by a second kernel: the result does not depend on which
+// block computed what. S comes from the sizes the host knows (plan()). Blocks
+// take the pieces of the experts with the most rows first, in alternating
+// direction from round to round, which evens out ragged experts: with 8
+// experts of 25,000 to 60,000 rows and three rounds, blocks' shares differ by
+// a few percent.
 #include "product_gemm.hpp"
 
 namespace moe {
 namespace {
 
+constexpr int kPlanCUs = 256;  // MI355X; the plan, hence the result, is the same on any device
+constexpr int kMaxSplit = 16;
+constexpr int64_t kMaxPieces = 4096;  // of a split: 1 GiB of partial sums
+constexpr int64_t kTileFloats = kTile * kTile;
+
+struct WgradPlan {
+    int64_t no, nh, tiles;  // tiles of O, of H, and of all experts
+    int32_t S;              // pieces of an expert's rows
+    int32_t bias_splits;    // pieces of its bias gradient's rows
+};
+
+// S minimises an estimate of the time in K-tiles (1.5 us each on MI355X): the
+// rounds of blocks, with 6 K-tiles for a tile's start and end, and for S > 1
+// the partial sums' way to memory and back, 512 KiB a tile (0.07), and the
+// second launch.
+WgradPlan plan(int32_t El, int64_t max_rows, int32_t O, int32_t H)
+{
+    WgradPlan p;
+    p.no = (O + kTile - 1) / kTile;
+    p.nh = (H + kTile - 1) / kTile;
+    p.tiles = El * p.no * p.nh;
+    const double nk = (double)max_rows / kTileK / El;
+    double best = 0;
+    p.S = 1;
+    for (int32_t s = 1; s <= kMaxSplit && (s == 1 || (nk >= 4 * s && p.tiles * s <= kMaxPieces)); ++s) {
+        const int64_t rounds = (p.tiles * s + kPlanCUs - 1) / kPlanCUs;
+        const double t = rounds * (nk / s + 6) + (s > 1 ? 0.07 * p.tiles * s + 4 : 0);
+        if (s == 1 || t < best) {
+            best = t;
+            p.S = s;
+        }
+    }
+    // the bias gradient reads rows of 512 columns per wave: about 1024 blocks,
+    // of 64 rows or more
+    const int64_t cols = (int64_t)El * ((O + 511) / 512);
+    int64_t b = 1024 / cols;
+    if (b > max_rows / El / 64)
+        b = max_rows / El / 64;
+    p.bias_splits = (int32_t)(b < 1 ? 1 : b);
+    return p;
+}
+
+size_t partial_bytes(const WgradPlan &p) { return p.S > 1 ? (size_t)(p.tiles * p.S * kTileFloats * 4) : 0; }
+
 struct WgradArgs {
     const uint16_t *gy, *x;
     const int32_t *off;
     void *gW;
-    int32_t El, max_rows, O, H;
+    float *partial;  // [El][S][tile][kTileFloats] in accumulator order
+    int32_t El, max_rows, O, H, S;
 };
 
-template <bool FP32, bool ACCUMULATE>
+// One tile to grad_W. Rows of 16 columns of O lie across the lanes.
+template <bool FP32, bool ACCUMULATE, class G>
+__device__ __forceinline__ void write_tile(const WgradArgs &p, const G &gemm, const Acc &acc, int32_t l, int32_t o0,
+                                           int32_t h0)
+{
+#pragma unroll
+    for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int32_t o = o0 + ha * 128 + gemm.wm * 64 + i * 16 + (gemm.lane & 15);
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb) {
+                const int64_t at = ((int64_t)l * p.O + o) * p.H + h0 + gemm.column(hb);
+                const int32_t left = p.H - h0 - gemm.column(hb), c4 = (gemm.lane >> 4) * 4;
+                if (FP32) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (o >= p.O || j * 16 + c4 >= left)
+                            continue;
+                        f32x4 v = acc[ha][hb][i][j];
+                        f32x4 *q = reinterpret_cast<f32x4 *>(static_cast<float *>(p.gW) + at + j * 16 + c4);
+                        if (ACCUMULATE)
+                            v += *q;
+                        *q = v;
+                    }
+                } else {
+                    const u32x4 v = to_rows(narrow(acc[ha][hb][i][0]), narrow(acc[ha][hb][i][1]));
+                    if (o < p.O && c4 * 2 < left)
+                        *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.gW) + at + c4 * 2) = v;
+                }
+            }
+        }
+}
+
+// accumulator fragment n of this lane within a partial tile
+__device__ __forceinline__ int64_t frag_at(int n, int wave, int lane) { return ((int64_t)(wave * 32 + n) * kWave + lane) * 4; }
+
+template <bool FP32, bool ACCUMULATE, bool SPLIT>
 __global__ __launch_bounds__(kGemmThreads, 2) void wgrad_kernel(WgradArgs p)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kGemmLdsBytes];
-    const int64_t no = (p.O + kTile - 1) / kTile, nh = (p.H + kTile - 1) / kTile;
+    __shared__ uint16_t by_rows[kMaxLocalExperts];  // experts, most rows first
+    const int64_t nh = (p.H + kTile - 1) / kTile, tp = ((p.O + kTile - 1) / kTile) * nh;
+    const int64_t units = p.El * (SPLIT ? p.S : 1) * tp;
+    const bool sorted = units > gridDim.x;
+    if (sorted) {
+        // rank by counting, from row counts staged where the tiles will lie
+        int32_t *n = reinterpret_cast<int32_t *>(lds);
+        for (int32_t l = threadIdx.x; l < p.El; l += kGemmThreads) {
+            const Rows r = expert_rows(p.off, l, p.max_rows);
+            n[l] = r.end - r.begin;
+        }
+        __syncthreads();
+        for (int32_t l = threadIdx.x; l < p.El; l += kGemmThreads) {
+            const int32_t mine = n[l];
+            int32_t rank = 0;
+            for (int32_t q = 0; q < p.El; ++q)
+                rank += n[q] > mine || (n[q] == mine && q < l);
+            by_rows[rank] = (uint16_t)l;
+        }
+        __syncthreads();
+    }
     Gemm<true, true> gemm;
     gemm.init_lane();
     const int32_t per_xcd = gridDim.x / 8;
     const int64_t slot = gridDim.x % 8 ? blockIdx.x : (int64_t)(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
-    for (int64_t u = slot; u < p.El * no * nh; u += gridDim.x) {
-        const int32_t h0 = (int32_t)(u % nh) * kTile, o0 = (int32_t)(u / nh % no) * kTile;
-        const int32_t l = (int32_t)(u / (nh * no));
+    for (int64_t round = 0; round * gridDim.x < units; ++round) {
+        const int64_t u = round * gridDim.x + (round & 1 ? gridDim.x - 1 - slot : slot);
+        if (u >= units)
+            continue;
+        const int64_t piece = u / tp, tile = u % tp;
+        const int32_t h0 = (int32_t)(tile % nh) * kTile, o0 = (int32_t)(tile / nh) * kTile;
+        const int32_t e = (int32_t)(SPLIT ? piece / p.S : piece), s = (int32_t)(SPLIT ? piece % p.S : 0);
+        const int32_t l = __builtin_amdgcn_readfirstlane(sorted ? by_rows[e] : e);
         const Rows r = expert_rows(p.off, l, p.max_rows);
-        const int32_t begin = __builtin_amdgcn_readfirstlane(r.begin);
-        const int32_t n = __builtin_amdgcn_readfirstlane(r.end - r.begin);
-        const int nk = (n + kTileK - 1) / kTileK;
-        gemm.A.init_strided(p.gy + (int64_t)begin * p.O + o0, n, p.O, p.O - o0, gemm.wave, gemm.lane);
-        gemm.B.init_strided(p.x + (int64_t)begin * p.H + h0, n, p.H, p.H - h0, gemm.wave, gemm.lane);
+        const int32_t rows = __builtin_amdgcn_readfirstlane(r.end - r.begin);
+        const int64_t all = (rows + (int64_t)kTileK - 1) / kTileK;
+        const int64_t t0 = SPLIT ? all * s / p.S : 0, t1 = SPLIT ? all * (s + 1) / p.S : all;
+        const int nk = (int)(t1 - t0);
+        if (SPLIT && nk == 0)
+            continue;
+        const int64_t first = __builtin_amdgcn_readfirstlane(r.begin) + t0 * kTileK;
+        const int64_t n = min(rows - t0 * kTileK, nk * (int64_t)kTileK);
+        gemm.A.init_strided(p.gy + first * p.O + o0, n, p.O, p.O - o0, gemm.wave, gemm.lane);
+        gemm.B.init_strided(p.x + first * p.H + h0, n, p.H, p.H - h0, gemm.wave, gemm.lane);
         Acc acc;
         gemm.start(lds, nk);
         gemm.run(lds, nk, acc);
+        if (SPLIT) {
+            float *q = p.partial + (((int64_t)l * p.S + s) * tp + tile) * kTileFloats;
 #pragma unroll
-        for (int ha = 0; ha < 2; ++ha)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int32_t o = o0 + ha * 128 + gemm.wm * 64 + i * 16 + (gemm.lane & 15);
-#pragma unroll
-                for (int hb = 0; hb < 2; ++hb) {
-                    const int64_t at = ((int64_t)l * p.O + o) * p.H + h0 + gemm.column(hb);
-                    const int32_t left = p.H - h0 - gemm.column(hb), c4 = (gemm.lane >> 4) * 4;
-                    if (FP32) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            if (o >= p.O || j * 16 + c4 >= left)
-                                continue;
-                            f32x4 v = acc[ha][hb][i][j];
-                            f32x4 *q = reinterpret_cast<f32x4 *>(static_cast<float *>(p.gW) + at + j * 16 + c4);
-                            if (ACCUMULATE)
-                                v += *q;
-                            *q = v;
-                        }
-                    } else {
-                        const u32x4 v = to_rows(narrow(acc[ha][hb][i][0]), narrow(acc[ha][hb][i][1]));
-                        if (o < p.O && c4 * 2 < left)
-                            *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.gW) + at + c4 * 2) = v;
-                    }
-                }
-            }
+            for (int i = 0; i < 32; ++i)
+                *reinterpret_cast<f32x4 *>(q + frag_at(i, gemm.wave, gemm.lane)) =
+                    acc[i >> 4][(i >> 3) & 1][(i >> 1) & 3][i & 1];
+        } else {
+            write_tile<FP32, ACCUMULATE>(p, gemm, acc, l, o0, h0);
+        }
         wait_loads<0>();
         slot_end();
     }
 }
 
-// A block sums 256 columns of one expert's rows.
-__global__ __launch_bounds__(256) void bias_grad_kernel(const uint16_t *__restrict__ gy,
-                                                        const int32_t *__restrict__ off, int32_t max_rows,
-                                                        int32_t O, bool accumulate, float *__restrict__ gb)
+// The pieces of one tile, added in ascending order.
+template <bool FP32, bool ACCUMULATE>
+__global__ __launch_bounds__(kGemmThreads, 2) void join_kernel(WgradArgs p)
 {
-    const int32_t o = blockIdx.x * 256 + threadIdx.x, l = blockIdx.y;
+    const int64_t nh = (p.H + kTile - 1) / kTile, tp = ((p.O + kTile - 1) / kTile) * nh;
+    Gemm<true, true> gemm;
+    gemm.init_lane();
+    const int32_t l = (int32_t)(blockIdx.x / tp);
+    const int64_t tile = blockIdx.x % tp;
+    const Rows r = expert_rows(p.off, l, p.max_rows);
+    const int64_t all = ((int64_t)r.end - r.begin + kTileK - 1) / kTileK;
+    Acc acc;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        acc[i >> 4][(i >> 3) & 1][(i >> 1) & 3][i & 1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int32_t s = 0; s < p.S; ++s) {
+        if (all * s / p.S == all * (s + 1) / p.S)
+            continue;
+        const float *q = p.partial + (((int64_t)l * p.S + s) * tp + tile) * kTileFloats;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            acc[i >> 4][(i >> 3) & 1][(i >> 1) & 3][i & 1] +=
+                __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(q + frag_at(i, gemm.wave, gemm.lane)));
+    }
+    write_tile<FP32, ACCUMULATE>(p, gemm, acc, l, (int32_t)(tile / nh) * kTile, (int32_t)(tile % nh) * kTile);
+}
+
+// Column sums of grad_y: a wave reads rows of 512 columns, 8 per lane, a block
+// takes piece blockIdx.z of one expert's rows. With one piece the result goes
+// to grad_bias, else to out[piece][El][O].
+constexpr int kBiasThreads = 256, kBiasWaves = kBiasThreads / kWave;
+__global__ __launch_bounds__(kBiasThreads) void bias_grad_kernel(const uint16_t *__restrict__ gy,
+                                                                 const int32_t *__restrict__ off, int32_t max_rows,
+                                                                 int32_t O, bool accumulate, float *__restrict__ out)
+{
+    __shared__ f32x4 part[kBiasWaves][kWave][2];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int32_t o = blockIdx.x * 512 + lane * 8, l = blockIdx.y;
     const Rows r = expert_rows(off, l, max_rows);
-    if (o >= O)
+    const int64_t n = (int64_t)r.end - r.begin;
+    const int64_t begin = r.begin + n * blockIdx.z / gridDim.z, end = r.begin + n * (blockIdx.z + 1) / gridDim.z;
+    f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = {0.f, 0.f, 0.f, 0.f};
+    if (o < O) {
+#pragma unroll 4
+        for (int64_t i = begin + wave; i < end; i += kBiasWaves) {
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(gy + i * O + o);
+            lo += widen(u32x2{v[0], v[1]});
+            hi += widen(u32x2{v[2], v[3]});
+        }
+    }
+    part[wave][lane][0] = lo;
+    part[wave][lane][1] = hi;
+    __syncthreads();
+    if (wave > 0 || o >= O)
+        return;
+#pragma unroll
+    for (int w = 1; w < kBiasWaves; ++w) {
+        lo += part[w][lane][0];
+        hi += part[w][lane][1];
+    }
+    float *q = out + ((int64_t)blockIdx.z * gridDim.y + l) * O + o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        q[e] = accumulate ? q[e] + lo[e] : lo[e];
+        q[4 + e] = accumulate ? q[4 + e] + hi[e] : hi[e];
+    }
+}
+
+__global__ __launch_bounds__(256) void bias_join_kernel(const float *__restrict__ part, int32_t splits, int64_t n,
+                                                        bool accumulate, float *__restrict__ gb)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n)
         return;
     float s = 0.f;
-    for (int64_t i = r.begin; i < r.end; ++i)
-        s += bf16_to_f32(gy[i * O + o]);
-    float *q = gb + (int64_t)l * O + o;
-    *q = accumulate ? *q + s : s;
+    for (int32_t k = 0; k < splits; ++k)
+        s += part[k * n + i];
+    gb[i] = accumulate ? gb[i] + s : s;
 }
 
 }  // namespace
 
-size_t wgrad_workspace_bytes(int32_t, int64_t, int32_t, int32_t) { return 0; }
+size_t wgrad_workspace_bytes(int32_t El, int64_t max_rows, int32_t O, int32_t H)
+{
+    const WgradPlan p = plan(El, max_rows, O, H);
+    return partial_bytes(p) + (p.bias_splits > 1 ? (size_t)p.bias_splits * El * O * sizeof(float) : 0);
+}
 
 hipError_t launch_expert_wgrad(const uint16_t *grad_y, const uint16_t *x, const int32_t *off,
                                int32_t El, int64_t max_rows, int32_t O, int32_t H, bool fp32,
-                               bool accumulate, void *grad_W, float *grad_bias, void *,
+                               bool accumulate, void *grad_W, float *grad_bias, void *workspace,
                                hipStream_t stream)
 {
     int device = 0, cus = 0;
@@ -98,20 +270,42 @@ hipError_t launch_expert_wgrad(const uint16_t *grad_y, const uint16_t *x, const 
         err = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
     if (err != hipSuccess)
         return err;
-    const int64_t tiles = (int64_t)El * ((O + kTile - 1) / kTile) * ((H + kTile - 1) / kTile);
-    const dim3 grid((unsigned)(tiles < cus ? tiles : cus));
-    const WgradArgs p = {grad_y, x, off, grad_W, El, (int32_t)max_rows, O, H};
-    if (accumulate)
-        hipLaunchKernelGGL((wgrad_kernel<true, true>), grid, dim3(kGemmThreads), 0, stream, p);
-    else if (fp32)
-        hipLaunchKernelGGL((wgrad_kernel<true, false>), grid, dim3(kGemmThreads), 0, stream, p);
-    else
-        hipLaunchKernelGGL((wgrad_kernel<false, false>), grid, dim3(kGemmThreads), 0, stream, p);
+    const WgradPlan plan_ = plan(El, max_rows, O, H);
+    const int64_t units = plan_.tiles * plan_.S;
+    const dim3 grid((unsigned)(units < cus ? units : cus)), block(kGemmThreads);
+    const WgradArgs p = {grad_y, x, off, grad_W, static_cast<float *>(workspace), El, (int32_t)max_rows, O, H,
+                         plan_.S};
+    if (plan_.S > 1) {
+        hipLaunchKernelGGL((wgrad_kernel<true, false, true>), grid, block, 0, stream, p);
+        if ((err = hipGetLastError()) != hipSuccess)
+            return err;
+        const dim3 joins((unsigned)plan_.tiles);
+        if (accumulate)
+            hipLaunchKernelGGL((join_kernel<true, true>), joins, block, 0, stream, p);
+        else if (fp32)
+            hipLaunchKernelGGL((join_kernel<true, false>), joins, block, 0, stream, p);
+        else
+            hipLaunchKernelGGL((join_kernel<false, false>), joins, block, 0, stream, p);
+    } else if (accumulate) {
+        hipLaunchKernelGGL((wgrad_kernel<true, true, false>), grid, block, 0, stream, p);
+    } else if (fp32) {
+        hipLaunchKernelGGL((wgrad_kernel<true, false, false>), grid, block, 0, stream, p);
+    } else {
+        hipLaunchKernelGGL((wgrad_kernel<false, false, false>), grid, block, 0, stream, p);
+    }
     err = hipGetLastError();
     if (err != hipSuccess || !grad_bias)
         return err;
-    hipLaunchKernelGGL(bias_grad_kernel, dim3((unsigned)((O + 255) / 256), (unsigned)El), dim3(256), 0, stream,
-                       grad_y, off, (int32_t)max_rows, O, accumulate, grad_bias);
+    float *part = reinterpret_cast<float *>(static_cast<char *>(workspace) + partial_bytes(plan_));
+    const int32_t splits = plan_.bias_splits;
+    hipLaunchKernelGGL(bias_grad_kernel, dim3((unsigned)((O + 511) / 512), (unsigned)El, (unsigned)splits),
+                       dim3(kBiasThreads), 0, stream, grad_y, off, (int32_t)max_rows, O, splits > 1 ? false : accumulate,
+                       splits > 1 ? part : grad_bias);
+    if ((err = hipGetLastError()) != hipSuccess || splits == 1)
+        return err;
+    const int64_t n = (int64_t)El * O;
+    hipLaunchKernelGGL(bias_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, part, splits, n,
+                       accumulate, grad_bias);
     return hipGetLastError();
 }
 
