@@ -108,6 +108,98 @@ __device__ __forceinline__ int owner_lane(uint32_t e)
     return VEC == 4 ? (int)((e >> 2) & (HW - 1)) : (int)(e & (HW - 1));
 }
 
+// The k largest of a token's keys, ties to the smaller id: lane j of the token
+// holds round j's id. NEXT also finds the best key left after them (0: none)
+// and its id, the same in all the token's lanes. Keys 0 are never selected.
+struct Selected {
+    uint32_t e, next_key, next_e;
+};
+template <int NSLOT, int VEC, int TPW, int NC, bool NEXT = false>
+__device__ __forceinline__ Selected select_topk(const uint32_t (&key)[NSLOT], int32_t k)
+{
+    using G = Group<TPW>;
+    constexpr int HW = G::HW;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int gl = lane & (HW - 1);
+    const int gbase = lane - gl;
+    // the lane's NC best entries
+    uint32_t c1k = key[0], c1i = slot_id<VEC, HW>(0, gl);
+    uint32_t c2k = 0u, c2i = 0xFFFFFFFFu, c3k = 0u, c3i = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 1; i < NSLOT; ++i)
+        insert_cand<NC>(key[i], slot_id<VEC, HW>(i, gl), c1k, c1i, c2k, c2i, c3k, c3i);
+
+    uint32_t my_e = 0;
+    for (int j = 0; j < k; ++j) {
+        const uint32_t best = G::max_u32(c1k);
+        uint32_t ew;
+        bool own;
+        if (TPW >= 4) {
+            // a token per row segment: the smallest id among the lanes holding
+            // the best key, by a minimum inside the segment; its lane owns it
+            ew = G::min_u32(c1k == best ? c1i : 0xFFFFFFFFu);
+            own = (c1k == best) & (c1i == ew);
+        } else {
+            const uint64_t holders = ballot64(c1k == best);
+            int owner;
+            bool unique;
+            if (TPW == 1)
+                unique = __popcll(holders) == 1;
+            else
+                unique = __popcll(holders & 0xFFFFFFFFull) == 1 && __popcll(holders >> 32) == 1;
+            if (unique) {
+                if (TPW == 1) {
+                    owner = __ffsll((unsigned long long)holders) - 1;
+                    ew = readlane_u32(c1i, owner);
+                } else {
+                    const int o0 = __ffsll((unsigned long long)(holders & 0xFFFFFFFFull)) - 1;
+                    const int o1 = 32 + __ffsll((unsigned long long)(holders >> 32)) - 1;
+                    const uint32_t e0 = readlane_u32(c1i, o0), e1 = readlane_u32(c1i, o1);
+                    owner = gbase == 0 ? o0 : o1;
+                    ew = gbase == 0 ? e0 : e1;
+                }
+            } else {  // several lanes of a token hold an equal key: the smallest id wins
+                ew = G::min_u32(c1k == best ? c1i : 0xFFFFFFFFu);
+                owner = gbase + owner_lane<VEC, HW>(ew);
+            }
+            own = lane == owner;
+        }
+        // lane j keeps round j's id: one writelane of the uniform id with one
+        // token per wave, a select per token otherwise
+        my_e = TPW == 1 ? writelane_u32(ew, j, my_e) : (gl == j ? ew : my_e);
+        // in the owner lane the candidate taken is (best, ew): the round's
+        // uniform key and id, so the pop below can overwrite c1 in place
+        const uint32_t gone_k = best, gone_i = ew;
+        c1k = own ? c2k : c1k;
+        c1i = own ? c2i : c1i;
+        if (NC == 3) {
+            c2k = own ? c3k : c2k;
+            c2i = own ? c3i : c2i;
+            c3k = own ? 0u : c3k;
+        } else {
+            c2k = own ? 0u : c2k;  // an empty slot's id is never read
+        }
+        if (own && c1k == 0u) {
+            // every candidate used: rescan the entries ranked below the last
+            // one taken from this lane
+            c1i = c2i = c3i = 0xFFFFFFFFu;
+#pragma unroll
+            for (int i = 0; i < NSLOT; ++i) {
+                const uint32_t id = slot_id<VEC, HW>(i, gl);
+                // bitwise, not short-circuit: a select per slot, no branches
+                const bool below = (key[i] < gone_k) | ((key[i] == gone_k) & (id > gone_i));
+                insert_cand<NC>(below ? key[i] : 0u, id, c1k, c1i, c2k, c2i, c3k, c3i);
+            }
+        }
+    }
+    Selected r = {my_e, 0u, 0u};
+    if (NEXT) {
+        r.next_key = G::max_u32(c1k);
+        r.next_e = G::min_u32(c1k == r.next_key ? c1i : 0xFFFFFFFFu);
+    }
+    return r;
+}
+
 // NSLOT keys per lane; VEC = 4 (16-byte loads) or 1 (4-byte loads); TPW
 // tokens per wave (2: each 32-lane half routes its own token, halving the
 // cost of the selection rounds per token); NC candidates per lane (2 or 3);
@@ -252,76 +344,7 @@ __device__ __forceinline__ void route_wave(
             key[i] = ((chosen >> gid[i]) & 1ull) ? key[i] : 0u;
     }
 
-    // the lane's NC best entries
-    uint32_t c1k = key[0], c1i = slot_id<VEC, HW>(0, gl);
-    uint32_t c2k = 0u, c2i = 0xFFFFFFFFu, c3k = 0u, c3i = 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = 1; i < NSLOT; ++i)
-        insert_cand<NC>(key[i], slot_id<VEC, HW>(i, gl), c1k, c1i, c2k, c2i, c3k, c3i);
-
-    uint32_t my_e = 0;
-    for (int j = 0; j < k; ++j) {
-        const uint32_t best = G::max_u32(c1k);
-        uint32_t ew;
-        bool own;
-        if (TPW >= 4) {
-            // a token per row segment: the smallest id among the lanes holding
-            // the best key, by a minimum inside the segment; its lane owns it
-            ew = G::min_u32(c1k == best ? c1i : 0xFFFFFFFFu);
-            own = (c1k == best) & (c1i == ew);
-        } else {
-            const uint64_t holders = ballot64(c1k == best);
-            int owner;
-            bool unique;
-            if (TPW == 1)
-                unique = __popcll(holders) == 1;
-            else
-                unique = __popcll(holders & 0xFFFFFFFFull) == 1 && __popcll(holders >> 32) == 1;
-            if (unique) {
-                if (TPW == 1) {
-                    owner = __ffsll((unsigned long long)holders) - 1;
-                    ew = readlane_u32(c1i, owner);
-                } else {
-                    const int o0 = __ffsll((unsigned long long)(holders & 0xFFFFFFFFull)) - 1;
-                    const int o1 = 32 + __ffsll((unsigned long long)(holders >> 32)) - 1;
-                    const uint32_t e0 = readlane_u32(c1i, o0), e1 = readlane_u32(c1i, o1);
-                    owner = gbase == 0 ? o0 : o1;
-                    ew = gbase == 0 ? e0 : e1;
-                }
-            } else {  // several lanes of a token hold an equal key: the smallest id wins
-                ew = G::min_u32(c1k == best ? c1i : 0xFFFFFFFFu);
-                owner = gbase + owner_lane<VEC, HW>(ew);
-            }
-            own = lane == owner;
-        }
-        // lane j keeps round j's id: one writelane of the uniform id with one
-        // token per wave, a select per token otherwise
-        my_e = TPW == 1 ? writelane_u32(ew, j, my_e) : (gl == j ? ew : my_e);
-        // in the owner lane the candidate taken is (best, ew): the round's
-        // uniform key and id, so the pop below can overwrite c1 in place
-        const uint32_t gone_k = best, gone_i = ew;
-        c1k = own ? c2k : c1k;
-        c1i = own ? c2i : c1i;
-        if (NC == 3) {
-            c2k = own ? c3k : c2k;
-            c2i = own ? c3i : c2i;
-            c3k = own ? 0u : c3k;
-        } else {
-            c2k = own ? 0u : c2k;  // an empty slot's id is never read
-        }
-        if (own && c1k == 0u) {
-            // every candidate used: rescan the entries ranked below the last
-            // one taken from this lane
-            c1i = c2i = c3i = 0xFFFFFFFFu;
-#pragma unroll
-            for (int i = 0; i < NSLOT; ++i) {
-                const uint32_t id = slot_id<VEC, HW>(i, gl);
-                // bitwise, not short-circuit: a select per slot, no branches
-                const bool below = (key[i] < gone_k) | ((key[i] == gone_k) & (id > gone_i));
-                insert_cand<NC>(below ? key[i] : 0u, id, c1k, c1i, c2k, c2i, c3k, c3i);
-            }
-        }
-    }
+    const uint32_t my_e = select_topk<NSLOT, VEC, TPW, NC>(key, k).e;
 
     // unbiased logits of the selected experts, straight from the row
     const bool mine = valid && gl < k;

@@ -564,9 +564,10 @@ moe_status_t moe_expert_return_slots(int32_t *slots);
  *     topk_groups groups take part, ties to the lower group.
  *   topk_idx = the k experts with the largest s among those, descending,
  *     ties to the smaller id. A NaN s ranks below every other.
- *   The order is that of s in exact arithmetic, to the resolution of 64-bit
- *     floating point: where two scores lie closer than float32 resolves,
- *     the token is ranked again in 64 bits.
+ *   The order is that of s in exact arithmetic: without a bias that of the
+ *     logits, and with one to the resolution of 64-bit floating point (where
+ *     two scores lie closer than float32 resolves, the token is ranked again
+ *     in 64 bits).
  *   topk_w[j] = scale * p[e_j] / sum_i p[e_i] with MOE_ROUTE_NORMALIZE, else
  *     scale * p[e_j]; computed in float32. Masked experts, which are selected
  *     only when too few others are left, get 0; a row whose selected scores

@@ -39,6 +39,9 @@ def route(logits, bias, k, n_groups=1, topk_groups=1, kind="softmax", normalize=
     T, E = l.shape
     p = scores(l, kind)
     s = np.where(l == -np.inf, -np.inf, p + (0.0 if bias is None else np.asarray(bias, np.float64)))
+    # both scores rise strictly with the logit, but not in 64 bits (sigmoid(40) and sigmoid(41) are both 1 there):
+    # without a bias the logit's order is the exact one
+    by = l if bias is None else s
     size = E // n_groups
     idx = np.empty((T, k), np.int32)
     for t in range(T):
@@ -46,12 +49,12 @@ def route(logits, bias, k, n_groups=1, topk_groups=1, kind="softmax", normalize=
         if topk_groups < n_groups:
             g = []
             for q in range(n_groups):
-                part = s[t, q * size:(q + 1) * size]
+                part = (s if top2 and size > 1 else by)[t, q * size:(q + 1) * size]
                 best = [part[i] for i in descending(part)]
                 g.append(best[0] + best[1] if top2 and size > 1 else best[0])
             chosen = set(descending(g)[:topk_groups])
             live = [e for e in range(E) if e // size in chosen]
-        order = descending([s[t, e] for e in live])
+        order = descending([by[t, e] for e in live])
         idx[t] = [live[i] for i in order[:k]]
     w = np.take_along_axis(p, idx.astype(np.int64), 1)
     if normalize:
