@@ -33,7 +33,8 @@ __device__ __forceinline__ float load_logit(const void *row, int32_t e)
     return static_cast<const float *>(row)[e];
 }
 
-// The row's logits in this lane's slots (slot_id's order), -inf past E.
+// The row's logits (or the biases) in this lane's slots (slot_id's order),
+// -inf past E.
 template <bool BF16, int NSLOT, int VEC, int HW>
 __device__ __forceinline__ void load_row(const void *row, int32_t E, int gl, bool valid, float (&l)[NSLOT])
 {
@@ -66,9 +67,13 @@ __device__ __forceinline__ void load_row(const void *row, int32_t E, int gl, boo
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 // A softmax's maximum (0 where the row has no finite logit, so that no
-// difference is NaN) and the reciprocal of its sum (0 for a sum of 0).
+// difference is NaN), that in the exponent's base, and the reciprocal of its
+// sum (0 for a sum of 0). m2 is rounded, which scales every term of the sum
+// and every score's numerator alike.
 struct Norm {
-    float m, inv;
+    float m, m2, inv;
+    // numerator of a softmax's score
+    __device__ __forceinline__ float term(float l) const { return __builtin_amdgcn_exp2f(fmaf(l, kLog2e, -m2)); }
 };
 template <int TPW, int NSLOT>
 __device__ __forceinline__ Norm softmax_norm(const float (&l)[NSLOT])
@@ -80,25 +85,26 @@ __device__ __forceinline__ Norm softmax_norm(const float (&l)[NSLOT])
         m = fmaxf(m, l[i]);
     m = G::max_f32(m);
     m = m == -INFINITY ? 0.f : m;
+    Norm n = {m, m * kLog2e, 0.f};
     float z = 0.f;
 #pragma unroll
     for (int i = 0; i < NSLOT; ++i)
-        z += fast_exp(l[i] - m);
+        z += n.term(l[i]);
     z = G::sum_f32(z);
-    return {m, z == 0.f ? 0.f : 1.f / z};
+    n.inv = z == 0.f ? 0.f : 1.f / z;
+    return n;
 }
 
-// Score of a logit. The sigmoid is the faster of two forms whose relative
-// error is a few kU; -inf gives 0 in both.
+// Score of a logit, plus b. -inf gives a score of 0.
 template <bool SIGMOID>
-__device__ __forceinline__ float score(float l, const Norm &n)
+__device__ __forceinline__ float score(float l, const Norm &n, float b)
 {
     if (SIGMOID)
-        return __builtin_amdgcn_rcpf(1.f + fast_exp(-l));
-    return fast_exp(l - n.m) * n.inv;
+        return __builtin_amdgcn_rcpf(1.f + fast_exp(-l)) + b;
+    return fmaf(n.term(l), n.inv, b);
 }
 
-// How far score() + b is from the exact sum. The exponent x is rounded twice
+// How far score() is from the exact sum. The exponent x is rounded twice
 // and scaled by a rounded constant (2.5 |x| kU in all), the exponential,
 // sum and reciprocal each by one or two steps; a sigmoid takes (1 - p) of its
 // exponential's share, a softmax's sum at most 43 kU more (its terms' shares
@@ -384,32 +390,44 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(ScoredArgs 
 
     float l[NSLOT];
     load_row<BF16, NSLOT, VEC, HW>(row, a.E, gl, valid, l);
-    Norm n = {0.f, 0.f};
+    Norm n = {0.f, 0.f, 0.f};
     const bool grouped = a.n_groups > 0, by_score = a.bias || (grouped && a.top2 && a.E > a.n_groups);
     if (!SIGMOID && (by_score || !a.normalize))
         n = softmax_norm<TPW>(l);
 
     uint32_t key[NSLOT];
-    auto set_keys = [&](bool scored) {
+    if (by_score) {
+        float b[NSLOT];
 #pragma unroll
-        for (int i = 0; i < NSLOT; ++i) {
-            const int32_t e = (int32_t)slot_id<VEC, HW>(i, gl);
-            float s = l[i];
-            if (scored) {
-                const float b = a.bias && e < a.E ? a.bias[e] : 0.f;
-                s = l[i] == -INFINITY ? -INFINITY : score<SIGMOID>(l[i], n) + b;
-            }
-            key[i] = valid && e < a.E ? score_key(s + 0.0f) : 0u;
+        for (int i = 0; i < NSLOT; ++i)
+            b[i] = 0.f;
+        if (a.bias)
+            load_row<false, NSLOT, VEC, HW>(a.bias, a.E, gl, true, b);
+        float low = l[0];
+#pragma unroll
+        for (int i = 1; i < NSLOT; ++i)
+            low = fminf(low, l[i]);
+        if (ballot64(low == -INFINITY)) {  // masked experts, or slots past E
+#pragma unroll
+            for (int i = 0; i < NSLOT; ++i)
+                l[i] = l[i] == -INFINITY ? -INFINITY : score<SIGMOID>(l[i], n, b[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NSLOT; ++i)
+                l[i] = score<SIGMOID>(l[i], n, b[i]);
         }
-    };
+    }
+#pragma unroll
+    for (int i = 0; i < NSLOT; ++i)
+        key[i] = valid && (int32_t)slot_id<VEC, HW>(i, gl) < a.E ? score_key(l[i] + 0.0f) : 0u;
     bool near = false;  // the float32 order is not certain
-    set_keys(by_score);
     if (grouped) {
         float taken;
         const float gap = keep_groups<NSLOT, VEC, TPW>(key, a.E, a.n_groups, a.topk_groups, a.top2, taken);
         near = by_score && gap <= 2.f * group_error<SIGMOID>(taken);
         if (by_score && !a.bias) {
             // groups by their scores, experts within them by their logits
+            load_row<BF16, NSLOT, VEC, HW>(row, a.E, gl, valid, l);
 #pragma unroll
             for (int i = 0; i < NSLOT; ++i)
                 key[i] = key[i] ? score_key(l[i] + 0.0f) : 0u;
@@ -418,29 +436,32 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(ScoredArgs 
     const Selected sel = select_topk<NSLOT, VEC, TPW, NC, true>(key, a.k);
     uint32_t my_e = sel.e;
     const bool mine = valid && gl < a.k;
-    float my_l = mine ? load_logit<BF16>(row, (int32_t)my_e) : -INFINITY;
+    float my_l = -INFINITY;
     if (a.bias) {
-        // each taken expert against the next one (the last against the best left)
-        auto at = [&](bool is, float lg, int32_t e, float &b, float &s, float &err) {
-            b = is ? a.bias[e] : 0.f;
-            const float p = score<SIGMOID>(lg, n);
-            s = lg == -INFINITY ? -INFINITY : p + b;
-            err = score_error<SIGMOID>(lg, p, s, n);
-        };
-        float b, s, err;
-        at(mine, my_l, (int32_t)my_e, b, s, err);
-        float l2 = __shfl_down(my_l, 1, kWave), b2 = __shfl_down(b, 1, kWave);
-        float s2 = __shfl_down(s, 1, kWave), err2 = __shfl_down(err, 1, kWave);
-        const bool some_left = sel.next_key != 0u;
-        if (gl == a.k - 1) {
-            const bool is = valid && some_left;
-            l2 = is ? load_logit<BF16>(row, (int32_t)sel.next_e) : -INFINITY;
-            at(is, l2, (int32_t)sel.next_e, b2, s2, err2);
-            // an equal pair here may hide a third expert next to it
-            near |= is && s - s2 <= err + err2;
-        } else if (mine) {
-            near |= (s - s2 <= err + err2) && !(my_l == l2 && b == b2);
+        // lane j: the expert of round j, lane k: the best one left
+        const bool is = mine || (valid && gl == a.k && sel.next_key != 0u);
+        const uint32_t e = gl == a.k ? sel.next_e : my_e;
+        float b = 0.f;
+        if (is) {
+            my_l = load_logit<BF16>(row, (int32_t)e);
+            b = a.bias[e];
         }
+        const float p = score<SIGMOID>(my_l, n, 0.f);
+        const float s = my_l == -INFINITY ? -INFINITY : score<SIGMOID>(my_l, n, b);
+        const float err = score_error<SIGMOID>(my_l, p, s, n);
+        // the next lane's, across the wave
+        constexpr int kShl1 = 0x130;
+        const float l2 = __uint_as_float(dpp::mov<kShl1>(__float_as_uint(my_l), 0u));
+        const float b2 = __uint_as_float(dpp::mov<kShl1>(__float_as_uint(b), 0u));
+        const float s2 = __uint_as_float(dpp::mov<kShl1>(__float_as_uint(s), __float_as_uint(-INFINITY)));
+        const float err2 = __uint_as_float(dpp::mov<kShl1>(__float_as_uint(err), 0u));
+        // An equal pair is ranked by its ids, but where it straddles the last
+        // place it may hide a third expert next to it. Masked ones (-inf) give
+        // NaN here: their order is known.
+        near |= mine && (s - s2 <= err + err2) && (gl == a.k - 1 || !(my_l == l2 && b == b2));
+        my_l = mine ? my_l : -INFINITY;
+    } else if (mine) {
+        my_l = load_logit<BF16>(row, (int32_t)my_e);
     }
     uint64_t again = ballot64(near && valid);
     while (again) {  // tokens of this wave, one after the other
@@ -474,7 +495,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(ScoredArgs 
     } else if (my_l == -INFINITY) {
         w = 0.f;
     } else {
-        w = SIGMOID ? 1.f / (1.f + expf(-my_l)) : expf(my_l - n.m) * n.inv;
+        w = SIGMOID ? 1.f / (1.f + expf(-my_l)) : n.term(my_l) * n.inv;
     }
     if (mine) {
         a.topk_idx[t * a.k + gl] = (int32_t)my_e;
@@ -523,7 +544,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_backward_kernel(Sc
         }
     }
     float l[NSLOT];
-    Norm n = {0.f, 0.f};
+    Norm n = {0.f, 0.f, 0.f};
     if (dense) {
         load_row<BF16, NSLOT, VEC, HW>(row, a.E, gl, valid, l);
         n = softmax_norm<TPW>(l);
@@ -540,7 +561,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_backward_kernel(Sc
     float gw;  // sum of gradient times weight
     float d;
     if (dense) {
-        const float p = fast_exp(le - n.m) * n.inv;
+        const float p = n.term(le) * n.inv;
         gw = G::sum_f32(g * p);
         d = g;
     } else {
@@ -576,7 +597,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_backward_kernel(Sc
             if (dense)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    v[i] = fast_exp(l[4 * q + i] - n.m) * c * (v[i] - gw);
+                    v[i] = n.term(l[4 * q + i]) * c * (v[i] - gw);
             if (valid && q * 4 * HW + 4 * gl < a.E) {
                 if (BF16)
                     __builtin_nontemporal_store(u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])},
@@ -591,7 +612,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_backward_kernel(Sc
             const int32_t x = i * HW + gl;
             float v = grads[x];
             if (dense)
-                v = fast_exp(l[i] - n.m) * c * (v - gw);
+                v = n.term(l[i]) * c * (v - gw);
             if (valid && x < a.E) {
                 if (BF16)
                     reinterpret_cast<uint16_t *>(out)[x] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu);
@@ -644,12 +665,12 @@ hipError_t launch(const ScoredGradArgs &args, hipStream_t stream)
 
 // The widths a wave is built for. Four logits per access where rows allow it
 // (E % 4 == 0 and aligned rows), so 4 per lane and slot quad; a short row
-// takes a part of the wave that holds its experts, its k ids and its groups.
+// takes a part of the wave that holds its experts, k + 1 ids and its groups.
 template <bool BF16, bool SIGMOID, class Args>
 hipError_t launch_width(const Args &a, bool vec4, int32_t groups, hipStream_t stream)
 {
     int seg = 4;
-    while (seg < (a.E + 3) / 4 || seg < a.k || seg < groups)
+    while (seg < (a.E + 3) / 4 || seg <= a.k || seg < groups)
         seg *= 2;
     if (vec4) {
         switch (seg) {
@@ -687,7 +708,7 @@ hipError_t launch_route_scored(const void *logits, const float *bias, int64_t T,
 {
     const ScoredArgs a = {logits, bias,    T,           E,       k,        n_groups, topk_groups,
                           o.top2, o.normalize, o.scale, topk_idx, topk_w};
-    const bool vec4 = E % 4 == 0 && (uintptr_t)logits % (o.bf16 ? 8 : 16) == 0;
+    const bool vec4 = E % 4 == 0 && (uintptr_t)logits % (o.bf16 ? 8 : 16) == 0 && (uintptr_t)bias % 16 == 0;
     return launch_type(a, vec4, n_groups, o, stream);
 }
 
