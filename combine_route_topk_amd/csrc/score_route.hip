@@ -266,10 +266,19 @@ __device__ __forceinline__ int wave_min(int v)
 // not there), NaN, -inf. Scores are finite or +inf.
 constexpr double kOut = -INFINITY, kNaNRank = -1.7e308, kMasked = -1.6e308;
 
-// Lane j returns the id of round j. NS slots of 64 experts.
+// Lane j returns the id of round j. NS slots of 64 experts. Without groups, no
+// expert whose score is below `least` is among the k best; the few others are
+// gathered, one for each lane, and placed by counting those ahead of them.
+// Rounds of a maximum over the wave, 64 bits at a time, took three times as
+// long, and are left for groups and for more than 64 candidates.
+struct Candidates {
+    double s[kWave];
+    int32_t e[kWave];
+};
 template <int NS, bool BF16, bool SIGMOID>
 __device__ __noinline__ int rank_exactly(const void *row, const float *__restrict__ bias, int32_t E, int32_t k,
-                                         int32_t n_groups, int32_t topk_groups, bool top2)
+                                         int32_t n_groups, int32_t topk_groups, bool top2, float least,
+                                         Candidates *__restrict__ cand)
 {
     const int lane = threadIdx.x & (kWave - 1);
     double s[NS], m = -INFINITY, z = 0.;
@@ -306,6 +315,35 @@ __device__ __noinline__ int rank_exactly(const void *row, const float *__restric
         if (v != -INFINITY)
             v = (SIGMOID ? v : v / z) + (bias ? (double)bias[e] : 0.);
         s[i] = v != v ? kNaNRank : (v == -INFINITY ? kMasked : v);
+    }
+    if (n_groups == 0) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const bool is = s[i] >= (double)least;
+            const uint64_t who = ballot64(is);
+            const int at = n + (int)count_below(who);
+            if (is && at < kWave) {
+                cand->s[at] = s[i];
+                cand->e[at] = i * kWave + lane;
+            }
+            n += __popcll(who);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (n >= k && n <= kWave) {
+            const double mine = lane < n ? cand->s[lane] : kOut;
+            const int32_t e = lane < n ? cand->e[lane] : 0x7FFFFFFF;
+            int ahead = 0;
+            for (int q = 0; q < n; ++q) {
+                const double o = cand->s[q];
+                ahead += o > mine || (o == mine && cand->e[q] < e);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (lane < n)
+                cand->e[ahead] = e;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            return cand->e[lane];
+        }
     }
     if (n_groups > 0) {
         const int32_t gsize = E / n_groups;
@@ -374,8 +412,10 @@ struct ScoredArgs {
 };
 
 template <int NSLOT, int VEC, int TPW, bool BF16, bool SIGMOID>
-__global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(ScoredArgs a)
+__global__ __launch_bounds__(kRouteThreads, 8) void route_scored_kernel(ScoredArgs a)
 {
+    // eight waves a SIMD: the 64-bit ranking spills for it, the rest does not
+    __shared__ Candidates cand[kWavesPerBlock];
     using G = Group<TPW>;
     constexpr int HW = G::HW;
     constexpr int NC = NSLOT >= 8 ? 3 : 2;
@@ -436,7 +476,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(ScoredArgs 
     const Selected sel = select_topk<NSLOT, VEC, TPW, NC, true>(key, a.k);
     uint32_t my_e = sel.e;
     const bool mine = valid && gl < a.k;
-    float my_l = -INFINITY;
+    float my_l = -INFINITY, least = -INFINITY;
     if (a.bias) {
         // lane j: the expert of round j, lane k: the best one left
         const bool is = mine || (valid && gl == a.k && sel.next_key != 0u);
@@ -460,10 +500,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(ScoredArgs 
         // NaN here: their order is known.
         near |= mine && (s - s2 <= err + err2) && (gl == a.k - 1 || !(my_l == l2 && b == b2));
         my_l = mine ? my_l : -INFINITY;
+        // the k best score at least the smallest of these, exactly
+        least = my_l == -INFINITY ? -INFINITY : s - err;
     } else if (mine) {
         my_l = load_logit<BF16>(row, (int32_t)my_e);
     }
     uint64_t again = ballot64(near && valid);
+    if (again)
+        least = -G::max_f32(mine ? -least : -INFINITY);
     while (again) {  // tokens of this wave, one after the other
         const int first = __ffsll((unsigned long long)again) - 1;
         const int base = first & ~(HW - 1);
@@ -471,7 +515,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(ScoredArgs 
         again &= ~lanes;
         const char *r = static_cast<const char *>(a.logits) + (t0 + base / HW) * row_bytes;
         constexpr int NS = (NSLOT * HW + kWave - 1) / kWave;
-        const int id = rank_exactly<NS, BF16, SIGMOID>(r, a.bias, a.E, a.k, a.n_groups, a.topk_groups, a.top2);
+        const int id = rank_exactly<NS, BF16, SIGMOID>(r, a.bias, a.E, a.k, a.n_groups, a.topk_groups, a.top2,
+                                                           __shfl(least, base, kWave), &cand[threadIdx.x / kWave]);
         const int got = __shfl(id, gl, kWave);
         if (gbase == base) {
             my_e = (uint32_t)got;
