@@ -6,18 +6,11 @@
 // A persistent block per CU takes tiles of 256 rows of one expert by 256
 // columns (gated: 128 gate columns and the 128 columns they gate, laid out
 // so that a lane holds both); product_gemm.hpp has the K loop.
+#include "product_epilogue.hpp"
 #include "product_gemm.hpp"
 
 namespace moe {
 namespace {
-
-struct ProductArgs {
-    const uint16_t *a;         // x, or grad_y (GRAD)
-    const int32_t *off;
-    const uint16_t *W, *bias, *residual, *pre_in;
-    uint16_t *pre_out, *out;
-    int32_t El, max_rows, K, N;  // N: columns before a gate doubles them
-};
 
 // Bias, activation, gate, residual (or the activation's gradient) on the
 // sums, and their one rounding. A group of 16 rows past the tile's last is
@@ -169,13 +162,13 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_kernel(ProductArgs p)
     }
 }
 
+constexpr int64_t kFewRowsEach = 16;
+
 template <bool GRAD>
 hipError_t launch(const ProductArgs &p, int32_t act, bool gated, hipStream_t stream)
 {
-    int device = 0, cus = 0;
-    hipError_t err = hipGetDevice(&device);
-    if (err == hipSuccess)
-        err = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
+    int cus = 0;
+    const hipError_t err = current_cus(&cus);
     if (err != hipSuccess)
         return err;
     const int kCols = gated && !GRAD ? kTile / 2 : kTile;
@@ -212,6 +205,8 @@ hipError_t launch_expert_product(const uint16_t *x, const int32_t *off, int32_t 
                                  bool gated, uint16_t *pre, uint16_t *y, hipStream_t stream)
 {
     const ProductArgs p = {x, off, W, bias, residual, nullptr, pre, y, El, (int32_t)max_rows, H, O};
+    if (max_rows <= kFewRowsEach * El)
+        return launch_product_few(p, act, gated, stream);
     return launch<false>(p, act, gated, stream);
 }
 

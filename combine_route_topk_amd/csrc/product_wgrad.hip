@@ -12,6 +12,7 @@
 // direction from round to round, which evens out ragged experts: with 8
 // experts of 25,000 to 60,000 rows and three rounds, blocks' shares differ by
 // a few percent.
+#include "product_epilogue.hpp"
 #include "product_gemm.hpp"
 
 namespace moe {
@@ -264,10 +265,8 @@ hipError_t launch_expert_wgrad(const uint16_t *grad_y, const uint16_t *x, const 
                                bool accumulate, void *grad_W, float *grad_bias, void *workspace,
                                hipStream_t stream)
 {
-    int device = 0, cus = 0;
-    hipError_t err = hipGetDevice(&device);
-    if (err == hipSuccess)
-        err = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
+    int cus = 0;
+    hipError_t err = current_cus(&cus);
     if (err != hipSuccess)
         return err;
     const WgradPlan plan_ = plan(El, max_rows, O, H);
