@@ -132,12 +132,19 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_kernel(ProductArgs p)
     // each XCD (blockIdx % 8) takes runs of consecutive tiles
     const int32_t per_xcd = gridDim.x / 8;
     const int64_t slot = gridDim.x % 8 ? blockIdx.x : (int64_t)(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
-    for (int64_t u = slot; u < row_tiles * nct; u += gridDim.x) {
-        const int32_t rt = (int32_t)(u / nct), n0 = (int32_t)(u % nct) * kCols;
+    // A last round that would leave half the blocks or more idle takes its
+    // tiles in two or four slices of rows, one for each block.
+    const int64_t tiles = row_tiles * nct, rest = tiles % gridDim.x, whole = tiles - rest;
+    const int32_t slices = rest * 4 <= gridDim.x ? 4 : (rest * 2 <= gridDim.x ? 2 : 1);
+    for (int64_t u = slot; u < whole + rest * slices; u += gridDim.x) {
+        const int64_t tile = u < whole ? u : whole + (u - whole) / slices;
+        const int32_t slice = u < whole ? 0 : (int32_t)((u - whole) % slices);
+        const int32_t most = u < whole ? kTile : kTile / slices;
+        const int32_t rt = (int32_t)(tile / nct), n0 = (int32_t)(tile % nct) * kCols;
         const int32_t l = __builtin_amdgcn_readfirstlane(tile_expert(first, p.El, rt));
         const Rows r = expert_rows(p.off, l, p.max_rows);
-        const int32_t row0 = __builtin_amdgcn_readfirstlane(r.begin + (rt - first[l]) * kTile);
-        const int32_t rows = __builtin_amdgcn_readfirstlane(min(kTile, r.end - row0));
+        const int32_t row0 = __builtin_amdgcn_readfirstlane(r.begin + (rt - first[l]) * kTile + slice * most);
+        const int32_t rows = __builtin_amdgcn_readfirstlane(min(most, r.end - row0));
         if (rows <= 0)
             continue;
         gemm.A.init(p.a + (int64_t)row0 * p.K, rows, p.K, gemm.wave, gemm.lane, 128, [](int j) { return j * 8; });
@@ -154,6 +161,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_kernel(ProductArgs p)
                         [](int j) { return (j >> 2) * 64 + (j & 3) * 8; });
         }
         Acc acc;
+        gemm.set_rows(rows);
         gemm.start(lds, nk);
         gemm.run(lds, nk, acc);
         epilogue<GRAD, GATED, ACT>(p, gemm, acc, l, row0, rows, n0);
@@ -162,7 +170,23 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_kernel(ProductArgs p)
     }
 }
 
-constexpr int64_t kFewRowsEach = 16;
+
+// Whether the kernel for few rows is the faster one, by the average rows of an
+// expert. On MI355X, in us, few against tiles:
+//   too few tiles for the CUs: 8 experts, 2048 by 2 x 768: 12 against 27 at 1
+//   row, 16 / 28 at 32, 25 / 28 at 48; 4 experts, 7168 by 7168: 79 / 105 at
+//   1 row, 97 / 107 at 16, 112 / 108 at 24;
+//   enough tiles, short K: 64 experts, 2048 by 2048: 103 / 128 at 1 row,
+//   124 / 127 at 16, 138 / 127 at 24;
+//   enough tiles, long K: 32 experts, 7168 by 2 x 2048: 319 / 307 at 4 rows,
+//   355 / 308 at 16 (one row each: 321 / 311).
+bool few_rows(int64_t max_rows, int32_t El, int32_t K, int64_t col_tiles)
+{
+    const int64_t tiles = (max_rows < El ? max_rows : El) * col_tiles;
+    if (tiles < 256)
+        return max_rows <= 20 * (int64_t)El;
+    return K < 4096 && max_rows <= 16 * (int64_t)El;
+}
 
 template <bool GRAD>
 hipError_t launch(const ProductArgs &p, int32_t act, bool gated, hipStream_t stream)
@@ -172,8 +196,9 @@ hipError_t launch(const ProductArgs &p, int32_t act, bool gated, hipStream_t str
     if (err != hipSuccess)
         return err;
     const int kCols = gated && !GRAD ? kTile / 2 : kTile;
-    const int64_t tiles = ((int64_t)p.max_rows / kTile + p.El) * ((p.N + kCols - 1) / kCols);
-    const dim3 grid((unsigned)(tiles < cus ? tiles : cus));
+    // four blocks a tile, for its slices
+    const int64_t units = 4 * ((int64_t)p.max_rows / kTile + p.El) * ((p.N + kCols - 1) / kCols);
+    const dim3 grid((unsigned)(units < cus ? units : cus));
 #define MOE_PRODUCT_LAUNCH(G, A)                                                                 \
     hipLaunchKernelGGL((product_kernel<GRAD, G, A>), grid, dim3(kGemmThreads), 0, stream, p);    \
     return hipGetLastError()
@@ -205,7 +230,7 @@ hipError_t launch_expert_product(const uint16_t *x, const int32_t *off, int32_t 
                                  bool gated, uint16_t *pre, uint16_t *y, hipStream_t stream)
 {
     const ProductArgs p = {x, off, W, bias, residual, nullptr, pre, y, El, (int32_t)max_rows, H, O};
-    if (max_rows <= kFewRowsEach * El)
+    if (few_rows(max_rows, El, H, (O + (gated ? kTile / 2 : kTile) - 1) / (gated ? kTile / 2 : kTile)))
         return launch_product_few(p, act, gated, stream);
     return launch<false>(p, act, gated, stream);
 }

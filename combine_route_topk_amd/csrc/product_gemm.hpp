@@ -267,6 +267,16 @@ struct Gemm {
     FragAddr<ASTR, 4> fa;
     FragAddr<BSTR, 2> fb;
     int wave, lane, wm, wn;
+    bool low, high;  // whether this wave's rows of A's first and second half are among the tile's
+
+    // A wave whose rows lie past the tile's `rows` takes its part in the loads
+    // and barriers only. (A loop of its own for full tiles, without the
+    // branches, spilled registers and was no faster.)
+    __device__ __forceinline__ void set_rows(int32_t rows)
+    {
+        low = rows > wm * 64;
+        high = rows > 128 + wm * 64;
+    }
 
     __device__ __forceinline__ void init_lane()
     {
@@ -320,19 +330,27 @@ struct Gemm {
         FragB b1;
         A.load(other + kHalfBytes, 1, t + 1, nk, wave);
         slot_a<ASTR>(fa, at, a);
-        mfmas(a, b0, acc[0][0]);
+        if (low)
+            mfmas(a, b0, acc[0][0]);
         slot_end();
         B.load(cur + 2 * kHalfBytes, 0, t + 2, nk, wave);
         slot_b<BSTR>(fb, at + 3 * kHalfBytes, b1);
-        mfmas(a, b1, acc[0][1]);
+        if (low)
+            mfmas(a, b1, acc[0][1]);
         slot_end();
         A.load(cur, 0, t + 2, nk, wave);
-        slot_a<ASTR>(fa, at + kHalfBytes, a);
-        mfmas(a, b1, acc[1][1]);
+        if (high) {
+            slot_a<ASTR>(fa, at + kHalfBytes, a);
+            mfmas(a, b1, acc[1][1]);
+        } else {
+            wait_loads<10>();
+            slot_end();
+        }
         slot_end();
         B.load(cur + 3 * kHalfBytes, 1, t + 2, nk, wave);
         slot_b<BSTR>(fb, then + 2 * kHalfBytes, next);
-        mfmas(a, b0, acc[1][0]);
+        if (high)
+            mfmas(a, b0, acc[1][0]);
         slot_end();
     }
 

@@ -156,6 +156,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void wgrad_kernel(WgradArgs p)
         gemm.A.init_strided(p.gy + first * p.O + o0, n, p.O, p.O - o0, gemm.wave, gemm.lane);
         gemm.B.init_strided(p.x + first * p.H + h0, n, p.H, p.H - h0, gemm.wave, gemm.lane);
         Acc acc;
+        gemm.set_rows(p.O - o0);
         gemm.start(lds, nk);
         gemm.run(lds, nk, acc);
         if (SPLIT) {
