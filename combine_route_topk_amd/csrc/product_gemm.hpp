@@ -318,12 +318,27 @@ struct Gemm {
         __builtin_amdgcn_s_setprio(0);
     }
 
+    // sum += this wave's quarter of a's rows, fragment wn, summed over k: a
+    // product with ones. Lanes L < 16 hold row wm * 64 + wn * 16 + L's.
+    __device__ __forceinline__ void add_rows(const FragA &a, f32x4 &sum) const
+    {
+        const __bf16 one = (__bf16)1.0f;
+        const bf16x8 ones = {one, one, one, one, one, one, one, one};
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+            if (wn == f)
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+                    sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, a.v[kk][f], sum, 0, 0, 0);
+    }
+
     // K-tile t, which lies in stage `cur`; b0 holds its first half of B, and
     // next receives the next K-tile's. A slot between two barriers holds either
     // reads and load starts or MFMAs, and the refill of a half tile starts a
     // barrier or more after every wave's reads of it are complete.
+    template <bool SUM>
     __device__ __forceinline__ void ktile(uint8_t *cur, uint8_t *other, int t, int nk, const FragB &b0, FragB &next,
-                                          Acc &acc) const
+                                          Acc &acc, f32x4 (&sum)[2], bool summed) const
     {
         const uint32_t at = lds_offset(cur), then = lds_offset(other);
         FragA a;
@@ -332,6 +347,8 @@ struct Gemm {
         slot_a<ASTR>(fa, at, a);
         if (low)
             mfmas(a, b0, acc[0][0]);
+        if (SUM && summed)
+            add_rows(a, sum[0]);
         slot_end();
         B.load(cur + 2 * kHalfBytes, 0, t + 2, nk, wave);
         slot_b<BSTR>(fb, at + 3 * kHalfBytes, b1);
@@ -342,6 +359,8 @@ struct Gemm {
         if (high) {
             slot_a<ASTR>(fa, at + kHalfBytes, a);
             mfmas(a, b1, acc[1][1]);
+            if (SUM && summed)
+                add_rows(a, sum[1]);
         } else {
             wait_loads<10>();
             slot_end();
@@ -356,8 +375,11 @@ struct Gemm {
 
     // The whole K loop; start() has been called. On return every wave has read
     // what it needs of LDS, and the loads still in flight bring only zeros.
-    __device__ __forceinline__ void run(uint8_t *lds, int nk, Acc &acc) const
+    // SUM: where `summed`, sum[h] receives the row sums of A's half h (add_rows).
+    template <bool SUM = false>
+    __device__ __forceinline__ void run(uint8_t *lds, int nk, Acc &acc, f32x4 (&sum)[2], bool summed) const
     {
+        sum[0] = sum[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int q = 0; q < 16; ++q)
 #pragma unroll
@@ -372,13 +394,18 @@ struct Gemm {
             slot_end();
         int t = 0;
         for (; t + 1 < nk; t += 2) {
-            ktile(s0, s1, t, nk, b0, b1, acc);
-            ktile(s1, s0, t + 1, nk, b1, b0, acc);
+            ktile<SUM>(s0, s1, t, nk, b0, b1, acc, sum, summed);
+            ktile<SUM>(s1, s0, t + 1, nk, b1, b0, acc, sum, summed);
         }
         if (t < nk)
-            ktile(s0, s1, t, nk, b0, b1, acc);
+            ktile<SUM>(s0, s1, t, nk, b0, b1, acc, sum, summed);
         if (!wm)
             slot_end();
+    }
+    __device__ __forceinline__ void run(uint8_t *lds, int nk, Acc &acc) const
+    {
+        f32x4 none[2];
+        run<false>(lds, nk, acc, none, false);
     }
 };
 

@@ -26,7 +26,6 @@ constexpr int64_t kTileFloats = kTile * kTile;
 struct WgradPlan {
     int64_t no, nh, tiles;  // tiles of O, of H, and of all experts
     int32_t S;              // pieces of an expert's rows
-    int32_t bias_splits;    // pieces of its bias gradient's rows
 };
 
 // S minimises an estimate of the time in K-tiles (1.5 us each on MI355X): the
@@ -50,13 +49,6 @@ WgradPlan plan(int32_t El, int64_t max_rows, int32_t O, int32_t H)
             p.S = s;
         }
     }
-    // the bias gradient reads rows of 512 columns per wave: about 1024 blocks,
-    // of 64 rows or more
-    const int64_t cols = (int64_t)El * ((O + 511) / 512);
-    int64_t b = 1024 / cols;
-    if (b > max_rows / El / 64)
-        b = max_rows / El / 64;
-    p.bias_splits = (int32_t)(b < 1 ? 1 : b);
     return p;
 }
 
@@ -66,9 +58,28 @@ struct WgradArgs {
     const uint16_t *gy, *x;
     const int32_t *off;
     void *gW;
+    float *gb;       // NULL: no bias gradient
     float *partial;  // [El][S][tile][kTileFloats] in accumulator order
+    float *partial_gb;  // [El][S][O]
     int32_t El, max_rows, O, H, S;
 };
+
+// Two groups of four float columns, 16 columns apart, of rows r = L % 16: a
+// becomes rows 0-7 (lanes with r < 8 the first group of row r, the others the
+// second of row r - 8), b rows 8-15 in the same way.
+__device__ __forceinline__ void to_lines(f32x4 &a, f32x4 &b)
+{
+    constexpr int kRowRor8 = 0x128;  // lane i of 16 <- lane i ^ 8
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t x = __float_as_uint(a[e]), y = __float_as_uint(b[e]);
+        // lanes 8-15 of a take b of the lane eight below, lanes 0-7 of b take a of the lane eight above
+        const uint32_t p = (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)y, kRowRor8, 0xF, 0xC, false);
+        const uint32_t q = (uint32_t)__builtin_amdgcn_update_dpp((int)y, (int)x, kRowRor8, 0xF, 0x3, false);
+        a[e] = __uint_as_float(p);
+        b[e] = __uint_as_float(q);
+    }
+}
 
 // One tile to grad_W. Rows of 16 columns of O lie across the lanes.
 template <bool FP32, bool ACCUMULATE, class G>
@@ -85,15 +96,23 @@ __device__ __forceinline__ void write_tile(const WgradArgs &p, const G &gemm, co
                 const int64_t at = ((int64_t)l * p.O + o) * p.H + h0 + gemm.column(hb);
                 const int32_t left = p.H - h0 - gemm.column(hb), c4 = (gemm.lane >> 4) * 4;
                 if (FP32) {
+                    // Whole 128-byte lines, rows 0-7 of the 16 in one access and 8-15 in
+                    // the other, written past the caches: 131 us against 138 for the
+                    // lanes' own pieces of 64 bytes (6 x 1536 x 7168, 4093 rows), and
+                    // 148 for those written past the caches.
+                    f32x4 v[2] = {acc[ha][hb][i][0], acc[ha][hb][i][1]};
+                    to_lines(v[0], v[1]);
+                    const int32_t r8 = gemm.lane & 7, c = (gemm.lane & 8) * 2 + c4;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        if (o >= p.O || j * 16 + c4 >= left)
+                        const int32_t row = o - (gemm.lane & 15) + j * 8 + r8;
+                        if (row >= p.O || c >= left)
                             continue;
-                        f32x4 v = acc[ha][hb][i][j];
-                        f32x4 *q = reinterpret_cast<f32x4 *>(static_cast<float *>(p.gW) + at + j * 16 + c4);
+                        f32x4 *q = reinterpret_cast<f32x4 *>(
+                            static_cast<float *>(p.gW) + ((int64_t)l * p.O + row) * p.H + h0 + gemm.column(hb) + c);
                         if (ACCUMULATE)
-                            v += *q;
-                        *q = v;
+                            v[j] += *q;
+                        __builtin_nontemporal_store(v[j], q);
                     }
                 } else {
                     const u32x4 v = to_rows(narrow(acc[ha][hb][i][0]), narrow(acc[ha][hb][i][1]));
@@ -104,10 +123,26 @@ __device__ __forceinline__ void write_tile(const WgradArgs &p, const G &gemm, co
         }
 }
 
+// The bias gradients of a tile's 256 columns, from the sums of grad_y that the
+// blocks of the first column of tiles make: grad_y's K-tile is in their
+// registers anyway, so 2 MFMAs in 18 cost them 6% and the other tiles nothing
+// (a kernel of its own, at the least, reads grad_y again).
+template <class G>
+__device__ __forceinline__ void write_bias(const G &gemm, const f32x4 (&sum)[2], float *q, int32_t o0, int32_t O,
+                                           bool accumulate)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int32_t o = o0 + h * 128 + gemm.wm * 64 + gemm.wn * 16 + gemm.lane;
+        if (gemm.lane < 16 && o < O)
+            q[o] = accumulate ? q[o] + sum[h][0] : sum[h][0];
+    }
+}
+
 // accumulator fragment n of this lane within a partial tile
 __device__ __forceinline__ int64_t frag_at(int n, int wave, int lane) { return ((int64_t)(wave * 32 + n) * kWave + lane) * 4; }
 
-template <bool FP32, bool ACCUMULATE, bool SPLIT>
+template <bool FP32, bool ACCUMULATE, bool SPLIT, bool BIAS>
 __global__ __launch_bounds__(kGemmThreads, 2) void wgrad_kernel(WgradArgs p)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kGemmLdsBytes];
@@ -156,9 +191,13 @@ __global__ __launch_bounds__(kGemmThreads, 2) void wgrad_kernel(WgradArgs p)
         gemm.A.init_strided(p.gy + first * p.O + o0, n, p.O, p.O - o0, gemm.wave, gemm.lane);
         gemm.B.init_strided(p.x + first * p.H + h0, n, p.H, p.H - h0, gemm.wave, gemm.lane);
         Acc acc;
+        f32x4 sum[2];
         gemm.set_rows(p.O - o0);
         gemm.start(lds, nk);
-        gemm.run(lds, nk, acc);
+        gemm.template run<BIAS>(lds, nk, acc, sum, h0 == 0);
+        if (BIAS && h0 == 0)
+            write_bias(gemm, sum, SPLIT ? p.partial_gb + ((int64_t)l * p.S + s) * p.O : p.gb + (int64_t)l * p.O, o0, p.O,
+                       !SPLIT && ACCUMULATE);
         if (SPLIT) {
             float *q = p.partial + (((int64_t)l * p.S + s) * tp + tile) * kTileFloats;
 #pragma unroll
@@ -197,60 +236,17 @@ __global__ __launch_bounds__(kGemmThreads, 2) void join_kernel(WgradArgs p)
             acc[i >> 4][(i >> 3) & 1][(i >> 1) & 3][i & 1] +=
                 __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(q + frag_at(i, gemm.wave, gemm.lane)));
     }
-    write_tile<FP32, ACCUMULATE>(p, gemm, acc, l, (int32_t)(tile / nh) * kTile, (int32_t)(tile % nh) * kTile);
-}
-
-// Column sums of grad_y: a wave reads rows of 512 columns, 8 per lane, a block
-// takes piece blockIdx.z of one expert's rows. With one piece the result goes
-// to grad_bias, else to out[piece][El][O].
-constexpr int kBiasThreads = 256, kBiasWaves = kBiasThreads / kWave;
-__global__ __launch_bounds__(kBiasThreads) void bias_grad_kernel(const uint16_t *__restrict__ gy,
-                                                                 const int32_t *__restrict__ off, int32_t max_rows,
-                                                                 int32_t O, bool accumulate, float *__restrict__ out)
-{
-    __shared__ f32x4 part[kBiasWaves][kWave][2];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int32_t o = blockIdx.x * 512 + lane * 8, l = blockIdx.y;
-    const Rows r = expert_rows(off, l, max_rows);
-    const int64_t n = (int64_t)r.end - r.begin;
-    const int64_t begin = r.begin + n * blockIdx.z / gridDim.z, end = r.begin + n * (blockIdx.z + 1) / gridDim.z;
-    f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = {0.f, 0.f, 0.f, 0.f};
-    if (o < O) {
-#pragma unroll 4
-        for (int64_t i = begin + wave; i < end; i += kBiasWaves) {
-            const u32x4 v = *reinterpret_cast<const u32x4 *>(gy + i * O + o);
-            lo += widen(u32x2{v[0], v[1]});
-            hi += widen(u32x2{v[2], v[3]});
-        }
-    }
-    part[wave][lane][0] = lo;
-    part[wave][lane][1] = hi;
-    __syncthreads();
-    if (wave > 0 || o >= O)
+    const int32_t o0 = (int32_t)(tile / nh) * kTile;
+    write_tile<FP32, ACCUMULATE>(p, gemm, acc, l, o0, (int32_t)(tile % nh) * kTile);
+    if (!p.gb || tile % nh != 0 || threadIdx.x >= kTile || o0 + (int32_t)threadIdx.x >= p.O)
         return;
-#pragma unroll
-    for (int w = 1; w < kBiasWaves; ++w) {
-        lo += part[w][lane][0];
-        hi += part[w][lane][1];
-    }
-    float *q = out + ((int64_t)blockIdx.z * gridDim.y + l) * O + o;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        q[e] = accumulate ? q[e] + lo[e] : lo[e];
-        q[4 + e] = accumulate ? q[4 + e] + hi[e] : hi[e];
-    }
-}
-
-__global__ __launch_bounds__(256) void bias_join_kernel(const float *__restrict__ part, int32_t splits, int64_t n,
-                                                        bool accumulate, float *__restrict__ gb)
-{
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n)
-        return;
-    float s = 0.f;
-    for (int32_t k = 0; k < splits; ++k)
-        s += part[k * n + i];
-    gb[i] = accumulate ? gb[i] + s : s;
+    const int32_t o = o0 + threadIdx.x;
+    float b = 0.f;
+    for (int32_t s = 0; s < p.S; ++s)
+        if (all * s / p.S != all * (s + 1) / p.S)
+            b += p.partial_gb[((int64_t)l * p.S + s) * p.O + o];
+    float *q = p.gb + (int64_t)l * p.O + o;
+    *q = ACCUMULATE ? *q + b : b;
 }
 
 }  // namespace
@@ -258,7 +254,7 @@ __global__ __launch_bounds__(256) void bias_join_kernel(const float *__restrict_
 size_t wgrad_workspace_bytes(int32_t El, int64_t max_rows, int32_t O, int32_t H)
 {
     const WgradPlan p = plan(El, max_rows, O, H);
-    return partial_bytes(p) + (p.bias_splits > 1 ? (size_t)p.bias_splits * El * O * sizeof(float) : 0);
+    return p.S > 1 ? partial_bytes(p) + (size_t)El * p.S * O * sizeof(float) : 0;
 }
 
 hipError_t launch_expert_wgrad(const uint16_t *grad_y, const uint16_t *x, const int32_t *off,
@@ -273,10 +269,18 @@ hipError_t launch_expert_wgrad(const uint16_t *grad_y, const uint16_t *x, const 
     const WgradPlan plan_ = plan(El, max_rows, O, H);
     const int64_t units = plan_.tiles * plan_.S;
     const dim3 grid((unsigned)(units < cus ? units : cus)), block(kGemmThreads);
-    const WgradArgs p = {grad_y, x, off, grad_W, static_cast<float *>(workspace), El, (int32_t)max_rows, O, H,
-                         plan_.S};
+    const WgradArgs p = {grad_y, x, off, grad_W, grad_bias, static_cast<float *>(workspace),
+                         reinterpret_cast<float *>(static_cast<char *>(workspace) + partial_bytes(plan_)),
+                         El, (int32_t)max_rows, O, H, plan_.S};
+#define MOE_WGRAD_LAUNCH(F, A, S)                                                              \
+    do {                                                                                       \
+        if (grad_bias)                                                                         \
+            hipLaunchKernelGGL((wgrad_kernel<F, A, S, true>), grid, block, 0, stream, p);      \
+        else                                                                                   \
+            hipLaunchKernelGGL((wgrad_kernel<F, A, S, false>), grid, block, 0, stream, p);     \
+    } while (0)
     if (plan_.S > 1) {
-        hipLaunchKernelGGL((wgrad_kernel<true, false, true>), grid, block, 0, stream, p);
+        MOE_WGRAD_LAUNCH(true, false, true);
         if ((err = hipGetLastError()) != hipSuccess)
             return err;
         const dim3 joins((unsigned)plan_.tiles);
@@ -287,25 +291,13 @@ hipError_t launch_expert_wgrad(const uint16_t *grad_y, const uint16_t *x, const 
         else
             hipLaunchKernelGGL((join_kernel<false, false>), joins, block, 0, stream, p);
     } else if (accumulate) {
-        hipLaunchKernelGGL((wgrad_kernel<true, true, false>), grid, block, 0, stream, p);
+        MOE_WGRAD_LAUNCH(true, true, false);
     } else if (fp32) {
-        hipLaunchKernelGGL((wgrad_kernel<true, false, false>), grid, block, 0, stream, p);
+        MOE_WGRAD_LAUNCH(true, false, false);
     } else {
-        hipLaunchKernelGGL((wgrad_kernel<false, false, false>), grid, block, 0, stream, p);
+        MOE_WGRAD_LAUNCH(false, false, false);
     }
-    err = hipGetLastError();
-    if (err != hipSuccess || !grad_bias)
-        return err;
-    float *part = reinterpret_cast<float *>(static_cast<char *>(workspace) + partial_bytes(plan_));
-    const int32_t splits = plan_.bias_splits;
-    hipLaunchKernelGGL(bias_grad_kernel, dim3((unsigned)((O + 511) / 512), (unsigned)El, (unsigned)splits),
-                       dim3(kBiasThreads), 0, stream, grad_y, off, (int32_t)max_rows, O, splits > 1 ? false : accumulate,
-                       splits > 1 ? part : grad_bias);
-    if ((err = hipGetLastError()) != hipSuccess || splits == 1)
-        return err;
-    const int64_t n = (int64_t)El * O;
-    hipLaunchKernelGGL(bias_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, part, splits, n,
-                       accumulate, grad_bias);
+#undef MOE_WGRAD_LAUNCH
     return hipGetLastError();
 }
 
