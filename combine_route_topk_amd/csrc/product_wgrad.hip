@@ -171,45 +171,67 @@ __global__ __launch_bounds__(kGemmThreads, 2) void wgrad_kernel(WgradArgs p)
     gemm.init_lane();
     const int32_t per_xcd = gridDim.x / 8;
     const int64_t slot = gridDim.x % 8 ? blockIdx.x : (int64_t)(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
-    for (int64_t round = 0; round * gridDim.x < units; ++round) {
-        const int64_t u = round * gridDim.x + (round & 1 ? gridDim.x - 1 - slot : slot);
-        if (u >= units)
-            continue;
-        const int64_t piece = u / tp, tile = u % tp;
-        const int32_t h0 = (int32_t)(tile % nh) * kTile, o0 = (int32_t)(tile / nh) * kTile;
-        const int32_t e = (int32_t)(SPLIT ? piece / p.S : piece), s = (int32_t)(SPLIT ? piece % p.S : 0);
-        const int32_t l = __builtin_amdgcn_readfirstlane(sorted ? by_rows[e] : e);
-        const Rows r = expert_rows(p.off, l, p.max_rows);
-        const int32_t rows = __builtin_amdgcn_readfirstlane(r.end - r.begin);
-        const int64_t all = (rows + (int64_t)kTileK - 1) / kTileK;
-        const int64_t t0 = SPLIT ? all * s / p.S : 0, t1 = SPLIT ? all * (s + 1) / p.S : all;
-        const int nk = (int)(t1 - t0);
-        if (SPLIT && nk == 0)
-            continue;
-        const int64_t first = __builtin_amdgcn_readfirstlane(r.begin) + t0 * kTileK;
-        const int64_t n = min(rows - t0 * kTileK, nk * (int64_t)kTileK);
-        gemm.A.init_strided(p.gy + first * p.O + o0, n, p.O, p.O - o0, gemm.wave, gemm.lane);
-        gemm.B.init_strided(p.x + first * p.H + h0, n, p.H, p.H - h0, gemm.wave, gemm.lane);
+    // One unit: a tile's piece s of expert l's rows.
+    struct Unit {
+        int64_t tile;
+        int32_t l, s, o0, h0, nk;
+    } next = {0, 0, 0, 0, 0, 0};
+    int64_t round = 0;
+    // Finds this block's next unit, points the operands at it and starts its
+    // first loads; false when there is none.
+    auto begin = [&]() -> bool {
+        for (; round * gridDim.x < units; ++round) {
+            const int64_t u = round * gridDim.x + (round & 1 ? gridDim.x - 1 - slot : slot);
+            if (u >= units)
+                continue;
+            const int64_t piece = u / tp;
+            next.tile = u % tp;
+            next.h0 = (int32_t)(next.tile % nh) * kTile;
+            next.o0 = (int32_t)(next.tile / nh) * kTile;
+            const int32_t e = (int32_t)(SPLIT ? piece / p.S : piece);
+            next.s = (int32_t)(SPLIT ? piece % p.S : 0);
+            next.l = __builtin_amdgcn_readfirstlane(sorted ? by_rows[e] : e);
+            const Rows r = expert_rows(p.off, next.l, p.max_rows);
+            const int32_t rows = __builtin_amdgcn_readfirstlane(r.end - r.begin);
+            const int64_t all = (rows + (int64_t)kTileK - 1) / kTileK;
+            const int64_t t0 = SPLIT ? all * next.s / p.S : 0, t1 = SPLIT ? all * (next.s + 1) / p.S : all;
+            next.nk = (int)(t1 - t0);
+            if (SPLIT && next.nk == 0)
+                continue;
+            const int64_t first = __builtin_amdgcn_readfirstlane(r.begin) + t0 * kTileK;
+            const int64_t n = min(rows - t0 * kTileK, next.nk * (int64_t)kTileK);
+            gemm.A.init_strided(p.gy + first * p.O + next.o0, n, p.O, p.O - next.o0, gemm.wave, gemm.lane);
+            gemm.B.init_strided(p.x + first * p.H + next.h0, n, p.H, p.H - next.h0, gemm.wave, gemm.lane);
+            gemm.set_rows(p.O - next.o0);
+            gemm.start(lds, next.nk);
+            ++round;
+            return true;
+        }
+        return false;
+    };
+    bool more = begin();
+    while (more) {
+        const Unit u = next;
         Acc acc;
         f32x4 sum[2];
-        gemm.set_rows(p.O - o0);
-        gemm.start(lds, nk);
-        gemm.template run<BIAS>(lds, nk, acc, sum, h0 == 0);
-        if (BIAS && h0 == 0)
-            write_bias(gemm, sum, SPLIT ? p.partial_gb + ((int64_t)l * p.S + s) * p.O : p.gb + (int64_t)l * p.O, o0, p.O,
-                       !SPLIT && ACCUMULATE);
+        gemm.template run<BIAS>(lds, u.nk, acc, sum, u.h0 == 0);
+        // the next unit's first loads run under this one's stores
+        more = begin();
+        if (BIAS && u.h0 == 0)
+            write_bias(gemm, sum, SPLIT ? p.partial_gb + ((int64_t)u.l * p.S + u.s) * p.O : p.gb + (int64_t)u.l * p.O,
+                       u.o0, p.O, !SPLIT && ACCUMULATE);
         if (SPLIT) {
-            float *q = p.partial + (((int64_t)l * p.S + s) * tp + tile) * kTileFloats;
+            float *q = p.partial + (((int64_t)u.l * p.S + u.s) * tp + u.tile) * kTileFloats;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 *reinterpret_cast<f32x4 *>(q + frag_at(i, gemm.wave, gemm.lane)) =
                     acc[i >> 4][(i >> 3) & 1][(i >> 1) & 3][i & 1];
         } else {
-            write_tile<FP32, ACCUMULATE>(p, gemm, acc, l, o0, h0);
+            write_tile<FP32, ACCUMULATE>(p, gemm, acc, u.l, u.o0, u.h0);
         }
-        wait_loads<0>();
-        slot_end();
     }
+    // loads past the last K-tile may still be on their way into LDS
+    wait_loads<0>();
 }
 
 // The pieces of one tile, added in ascending order.
