@@ -82,9 +82,7 @@ __device__ void few_tile(const ProductArgs &p, int32_t l, int32_t row0, int32_t 
 #pragma unroll
         for (int m = 0; m < MT; ++m)
             s.c[g][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    constexpr int U = 2;
     const int32_t full = p.K / kFewStep;  // rounds that need no check of k
-#pragma unroll U
     for (int32_t i = 0; i < full; ++i)
         few_step<MT, NG>(w, x, woff, xoff, (uint32_t)i * (kFewStep * 2), s);
     if (full * kFewStep < p.K) {
@@ -144,10 +142,11 @@ __global__ __launch_bounds__(kFewThreads, 4) void product_few_kernel(ProductArgs
     const int32_t row_tiles = plan_row_tiles<kFewThreads, kFewRows>(p.off, p.El, p.max_rows, first);
     const int64_t nct = (p.N + kFewCols - 1) / kFewCols;
     for (int64_t u = blockIdx.x; u < row_tiles * nct; u += gridDim.x) {
-        const int32_t rt = (int32_t)(u / nct), n0 = (int32_t)(u % nct) * kFewCols;
+        const int32_t rt = __builtin_amdgcn_readfirstlane((int32_t)(u / nct));
+        const int32_t n0 = __builtin_amdgcn_readfirstlane((int32_t)(u % nct)) * kFewCols;
         const int32_t l = __builtin_amdgcn_readfirstlane(tile_expert(first, p.El, rt));
         const Rows r = expert_rows(p.off, l, p.max_rows);
-        const int32_t row0 = __builtin_amdgcn_readfirstlane(r.begin + (rt - first[l]) * kFewRows);
+        const int32_t row0 = __builtin_amdgcn_readfirstlane((int32_t)(r.begin + (int64_t)(rt - first[l]) * kFewRows));
         const int32_t rows = __builtin_amdgcn_readfirstlane(min(kFewRows, r.end - row0));
         if (rows <= 16)
             few_tile<1, NG, GATED, ACT>(p, l, row0, rows, n0, part);

@@ -156,8 +156,10 @@ struct FragB {
     bf16x8 v[2][2];
 };
 
-#define MOE_READ(d, a, o) "ds_read_b128 %" #d ", %" #a " offset:" #o "\n\t"
-#define MOE_READ_TR(d, a, o) "ds_read_b64_tr_b16 %" #d ", %" #a " offset:" #o "\n\t"
+// The half tile's offset within its stage is part of the instruction, so that
+// one address register serves a stage's four.
+#define MOE_READ(d, a, o) "ds_read_b128 %" #d ", %" #a " offset:%[half]+" #o "\n\t"
+#define MOE_READ_TR(d, a, o) "ds_read_b64_tr_b16 %" #d ", %" #a " offset:%[half]+" #o "\n\t"
 // destination numbers d.., address numbers a..
 #define MOE_READ_A(d0, d1, d2, d3, d4, d5, d6, d7, a0, a1)                                              \
     MOE_READ(d0, a0, 0) MOE_READ(d1, a0, 2048) MOE_READ(d2, a0, 4096) MOE_READ(d3, a0, 6144)            \
@@ -198,38 +200,39 @@ struct FragAddr {
 };
 
 // The slot that reads a half of B, and the one that reads a half of A.
-template <bool STRIDED>
-__device__ __forceinline__ void slot_b(const FragAddr<STRIDED, 2> &fb, uint32_t half, FragB &b)
+template <int HALF, bool STRIDED>
+__device__ __forceinline__ void slot_b(const FragAddr<STRIDED, 2> &fb, uint32_t stage, FragB &b)
 {
     if constexpr (STRIDED) {
         TrFrag q[2];
         asm volatile(MOE_READ_TR4(0, 1, 2, 3, 8) MOE_READ_TR4(4, 5, 6, 7, 9) MOE_SLOT_END
                      : MOE_OUT_TR4(q[0]), MOE_OUT_TR4(q[1])
-                     : "v"(half + fb.a[0]), "v"(half + fb.a[1])
+                     : "v"(stage + fb.a[0]), "v"(stage + fb.a[1]), [half] "n"(HALF * kHalfBytes)
                      : "memory");
         from_tr(q, b);
     } else {
         asm volatile(MOE_READ_B(0, 1, 2, 3, 4, 5) MOE_SLOT_END
                      : MOE_OUT_B(b)
-                     : "v"(half + fb.a[0]), "v"(half + fb.a[1])
+                     : "v"(stage + fb.a[0]), "v"(stage + fb.a[1]), [half] "n"(HALF * kHalfBytes)
                      : "memory");
     }
 }
-template <bool STRIDED>
-__device__ __forceinline__ void slot_a(const FragAddr<STRIDED, 4> &fa, uint32_t half, FragA &a)
+template <int HALF, bool STRIDED>
+__device__ __forceinline__ void slot_a(const FragAddr<STRIDED, 4> &fa, uint32_t stage, FragA &a)
 {
     if constexpr (STRIDED) {
         TrFrag q[4];
         asm volatile(MOE_READ_TR4(0, 1, 2, 3, 16) MOE_READ_TR4(4, 5, 6, 7, 17) MOE_READ_TR4(8, 9, 10, 11, 18)
                          MOE_READ_TR4(12, 13, 14, 15, 19) MOE_SLOT_END
                      : MOE_OUT_TR4(q[0]), MOE_OUT_TR4(q[1]), MOE_OUT_TR4(q[2]), MOE_OUT_TR4(q[3])
-                     : "v"(half + fa.a[0]), "v"(half + fa.a[1]), "v"(half + fa.a[2]), "v"(half + fa.a[3])
+                     : "v"(stage + fa.a[0]), "v"(stage + fa.a[1]), "v"(stage + fa.a[2]), "v"(stage + fa.a[3]),
+                       [half] "n"(HALF * kHalfBytes)
                      : "memory");
         from_tr(q, a);
     } else {
         asm volatile(MOE_READ_A(0, 1, 2, 3, 4, 5, 6, 7, 8, 9) MOE_SLOT_END
                      : MOE_OUT_A(a)
-                     : "v"(half + fa.a[0]), "v"(half + fa.a[1])
+                     : "v"(stage + fa.a[0]), "v"(stage + fa.a[1]), [half] "n"(HALF * kHalfBytes)
                      : "memory");
     }
 }
@@ -344,20 +347,20 @@ struct Gemm {
         FragA a;
         FragB b1;
         A.load(other + kHalfBytes, 1, t + 1, nk, wave);
-        slot_a<ASTR>(fa, at, a);
+        slot_a<0>(fa, at, a);
         if (low)
             mfmas(a, b0, acc[0][0]);
         if (SUM && summed)
             add_rows(a, sum[0]);
         slot_end();
         B.load(cur + 2 * kHalfBytes, 0, t + 2, nk, wave);
-        slot_b<BSTR>(fb, at + 3 * kHalfBytes, b1);
+        slot_b<3>(fb, at, b1);
         if (low)
             mfmas(a, b1, acc[0][1]);
         slot_end();
         A.load(cur, 0, t + 2, nk, wave);
         if (high) {
-            slot_a<ASTR>(fa, at + kHalfBytes, a);
+            slot_a<1>(fa, at, a);
             mfmas(a, b1, acc[1][1]);
             if (SUM && summed)
                 add_rows(a, sum[1]);
@@ -367,7 +370,7 @@ struct Gemm {
         }
         slot_end();
         B.load(cur + 3 * kHalfBytes, 1, t + 2, nk, wave);
-        slot_b<BSTR>(fb, then + 2 * kHalfBytes, next);
+        slot_b<2>(fb, then, next);
         if (high)
             mfmas(a, b0, acc[1][0]);
         slot_end();
@@ -389,7 +392,7 @@ struct Gemm {
         wait_loads<10>();
         slot_end();
         FragB b0, b1;
-        slot_b<BSTR>(fb, lds_offset(s0 + 2 * kHalfBytes), b0);
+        slot_b<2>(fb, lds_offset(s0), b0);
         if (wm)  // the second group of waves starts half a phase later
             slot_end();
         int t = 0;

@@ -186,10 +186,10 @@ __global__ __launch_bounds__(kGemmThreads, 2) void wgrad_kernel(WgradArgs p)
                 continue;
             const int64_t piece = u / tp;
             next.tile = u % tp;
-            next.h0 = (int32_t)(next.tile % nh) * kTile;
-            next.o0 = (int32_t)(next.tile / nh) * kTile;
+            next.h0 = __builtin_amdgcn_readfirstlane((int32_t)(next.tile % nh)) * kTile;
+            next.o0 = __builtin_amdgcn_readfirstlane((int32_t)(next.tile / nh)) * kTile;
             const int32_t e = (int32_t)(SPLIT ? piece / p.S : piece);
-            next.s = (int32_t)(SPLIT ? piece % p.S : 0);
+            next.s = SPLIT ? __builtin_amdgcn_readfirstlane((int32_t)(piece % p.S)) : 0;
             next.l = __builtin_amdgcn_readfirstlane(sorted ? by_rows[e] : e);
             const Rows r = expert_rows(p.off, next.l, p.max_rows);
             const int32_t rows = __builtin_amdgcn_readfirstlane(r.end - r.begin);
