@@ -74,8 +74,10 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, const G &gemm, co
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            dz[j][e] = v[j][e] * u[j][e] * act_grad<ACT>(z[j][e]);
-                            du[j][e] = v[j][e] * act<ACT>(z[j][e]);
+                            float f, df;
+                            act_and_grad<ACT>(z[j][e], f, df);
+                            dz[j][e] = v[j][e] * u[j][e] * df;
+                            du[j][e] = v[j][e] * f;
                         }
                     out.store(m, col[q], dz);
                     out.store(m, col[q], du, N2);
@@ -86,8 +88,11 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, const G &gemm, co
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                v[j][e] *= act_grad<ACT>(z[j][e]);
+                            for (int e = 0; e < 4; ++e) {
+                                float f, df;
+                                act_and_grad<ACT>(z[j][e], f, df);
+                                v[j][e] *= df;
+                            }
                     }
                     out.store(m, col[q], v);
                 } else {

@@ -91,7 +91,7 @@ __device__ __forceinline__ int32_t tile_expert(const int32_t *first, int32_t El,
     return lo;
 }
 
-// act(z) and act'(z) in float32, ACT a moe_act value. Arguments of the
+// act(z) in float32, ACT a moe_act value. Arguments of the
 // exponentials are bounded where a product with an overflowed factor would
 // give NaN: beyond |z| = 30 both GELUs' cdf and derivative are 0 or 1 in
 // float32, and SiLU's are once |z| > 104.
@@ -129,24 +129,36 @@ __device__ __forceinline__ float act(float z)
     }
 }
 
+// act(z) and act'(z) together: they share their exponential.
 template <int ACT>
-__device__ __forceinline__ float act_grad(float z)
+__device__ __forceinline__ void act_and_grad(float z, float &f, float &df)
 {
     switch (ACT) {
-    case kActRelu: return z > 0.f ? 1.f : (z != z ? z : 0.f);
+    case kActRelu:
+        f = act<ACT>(z);
+        df = z > 0.f ? 1.f : (z != z ? z : 0.f);
+        return;
     case kActSilu: {
-        const float b = fminf(fmaxf(z, -104.f), 104.f), p = sigmoid(b);
-        return p * (1.f + b * (1.f - p));
+        const float p = sigmoid(z);
+        f = z * p;
+        df = p * (1.f + fminf(fmaxf(z, -104.f), 104.f) * (1.f - p));
+        return;
     }
     case kActGelu: {
-        const float b = fminf(fmaxf(z, -30.f), 30.f);
-        return 0.5f * erfcf(-b * kSqrtHalf) + b * __builtin_amdgcn_exp2f(-0.72134752044448170f * b * b) * kInvSqrt2Pi;
+        const float b = fminf(fmaxf(z, -30.f), 30.f), cdf = 0.5f * erfcf(-b * kSqrtHalf);
+        f = z * cdf;
+        df = cdf + b * __builtin_amdgcn_exp2f(-0.72134752044448170f * b * b) * kInvSqrt2Pi;
+        return;
     }
     case kActGeluTanh: {
         const float b = fminf(fmaxf(z, -30.f), 30.f), p = gelu_tanh_cdf(b);
-        return p + 2.f * b * p * (1.f - p) * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * b * b);
+        f = z * p;
+        df = p + 2.f * b * p * (1.f - p) * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * b * b);
+        return;
     }
-    default: return 1.f;
+    default:
+        f = z;
+        df = 1.f;
     }
 }
 
