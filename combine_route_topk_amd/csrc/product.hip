@@ -53,72 +53,89 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, const G &gemm, co
     TileRows pre;
     if (!GRAD && p.pre_out)
         pre.init(p.pre_out, row0, rows, wide, gemm.lane);
+    // What a group of 16 rows reads (pre, or the residual) is fetched while the
+    // group before it is computed: a wave has only one other on its SIMD to
+    // hide that latency.
+    constexpr int NF = GRAD && GATED ? 2 : 1;
+    const bool reads = GRAD ? (GATED || p.pre_in) : p.residual != nullptr;
+    u32x4 ahead[2][NP][NF];
+    auto row_of = [&](int s) { return (s >> 2) * 128 + gemm.wm * 64 + (s & 3) * 16; };
+    auto fetch = [&](int s) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+        for (int q = 0; q < NP; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int32_t m = h * 128 + gemm.wm * 64 + i * 16;
-            if (m >= rows)
-                continue;
+            for (int f = 0; f < NF; ++f)
+                ahead[s & 1][q][f] = aux.fetch(row_of(s), col[q], f * N2);
+    };
+    if (reads)
+        fetch(0);
 #pragma unroll
-            for (int q = 0; q < NP; ++q) {
-                f32x4 v[2];
+    for (int s = 0; s < 8; ++s) {
+        const int h = s >> 2, i = s & 3;
+        if (reads && s < 7)
+            fetch(s + 1);
+        const int32_t m = row_of(s);
+        if (m >= rows)
+            continue;
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            f32x4 v[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                v[j] = PAIR ? acc[h][j][i][0] : acc[h][q][i][j];
+            if (GRAD && GATED) {
+                f32x4 z[2], u[2], dz[2], du[2];
+                TileRows::unpack(ahead[s & 1][q][0], z);
+                TileRows::unpack(ahead[s & 1][q][NF - 1], u);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    v[j] = PAIR ? acc[h][j][i][0] : acc[h][q][i][j];
-                if (GRAD && GATED) {
-                    f32x4 z[2], u[2], dz[2], du[2];
-                    aux.load(m, col[q], z);
-                    aux.load(m, col[q], u, N2);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float f, df;
+                        act_and_grad<ACT>(z[j][e], f, df);
+                        dz[j][e] = v[j][e] * u[j][e] * df;
+                        du[j][e] = v[j][e] * f;
+                    }
+                out.store(m, col[q], dz);
+                out.store(m, col[q], du, N2);
+            } else if (GRAD) {
+                if (p.pre_in) {
+                    f32x4 z[2];
+                    TileRows::unpack(ahead[s & 1][q][0], z);
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float f, df;
                             act_and_grad<ACT>(z[j][e], f, df);
-                            dz[j][e] = v[j][e] * u[j][e] * df;
-                            du[j][e] = v[j][e] * f;
+                            v[j][e] *= df;
                         }
-                    out.store(m, col[q], dz);
-                    out.store(m, col[q], du, N2);
-                } else if (GRAD) {
-                    if (p.pre_in) {
-                        f32x4 z[2];
-                        aux.load(m, col[q], z);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float f, df;
-                                act_and_grad<ACT>(z[j][e], f, df);
-                                v[j][e] *= df;
-                            }
-                    }
-                    out.store(m, col[q], v);
-                } else {
-                    f32x4 g[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        v[j] += b[q][j];
-                        g[j] = PAIR ? acc[h][j][i][1] + bu[q][j] : f32x4{};
-                    }
-                    if (p.pre_out) {
-                        pre.store(m, col[q], v);
-                        if (PAIR)
-                            pre.store(m, col[q], g, N2);
-                    }
-                    f32x4 r[2] = {};
-                    if (p.residual)
-                        aux.load(m, col[q], r);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[j][e] = (PAIR ? act<ACT>(v[j][e]) * g[j][e] : act<ACT>(v[j][e])) + r[j][e];
-                    out.store(m, col[q], v);
                 }
+                out.store(m, col[q], v);
+            } else {
+                f32x4 g[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    v[j] += b[q][j];
+                    g[j] = PAIR ? acc[h][j][i][1] + bu[q][j] : f32x4{};
+                }
+                if (p.pre_out) {
+                    pre.store(m, col[q], v);
+                    if (PAIR)
+                        pre.store(m, col[q], g, N2);
+                }
+                f32x4 r[2] = {};
+                if (p.residual)
+                    TileRows::unpack(ahead[s & 1][q][0], r);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[j][e] = (PAIR ? act<ACT>(v[j][e]) * g[j][e] : act<ACT>(v[j][e])) + r[j][e];
+                out.store(m, col[q], v);
             }
         }
+    }
 }
 
 template <bool GRAD, bool GATED, int ACT>

@@ -454,7 +454,7 @@ __device__ __forceinline__ u32x2 narrow(f32x4 v) { return {pack_bf16x2(v[0], v[1
 // A tile's rows of a [rows][ld] bf16 tensor, through a descriptor that ends
 // with the tile's last row: pairs of column groups as above, this lane's eight
 // consecutive columns at byte offset col (kOutside or more past the width) of
-// row m + lane % 16, m uniform and below the tile's rows. The stores carry no
+// row m + lane % 16, m uniform. The stores carry no
 // scalar offset: a 16-byte store with one, followed at once by an instruction
 // that writes its last data register, stored the new value in some lanes on
 // gfx950, and the compiler keeps the two apart only where there is none.
@@ -468,12 +468,16 @@ struct TileRows {
         ld2 = (uint32_t)ld * 2;
         lane_row = (uint32_t)(lane & 15) * ld2;
     }
-    __device__ __forceinline__ void load(uint32_t m, uint32_t col, f32x4 (&v)[2], uint32_t half = 0) const
+    // any m: past the tile's rows it gives zeros
+    __device__ __forceinline__ u32x4 fetch(uint32_t m, uint32_t col, uint32_t half = 0) const
+    {
+        return __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_row + col + (m * ld2 + half), 0, 0));
+    }
+    __device__ __forceinline__ static void unpack(u32x4 raw, f32x4 (&v)[2])
     {
         u32x2 a, b;
-        from_rows(__builtin_bit_cast(
-                      u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_row + col, m * ld2 + half, 0)),
-                  a, b);
+        from_rows(raw, a, b);
         v[0] = widen(a);
         v[1] = widen(b);
     }
