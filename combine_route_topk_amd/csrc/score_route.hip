@@ -115,12 +115,14 @@ __device__ __forceinline__ float score_error(float l, float p, float s, const No
     const float share = SIGMOID ? (1.f - p) * (2.5f * fabsf(l) + 2.f) + 4.f : 2.5f * fabsf(l - n.m) + 50.f;
     return (p * share + fabsf(s)) * kU + 2.3509887e-38f;
 }
-// The same for a group's score: p share is at most 5.1 for a sigmoid and
-// 51 for a softmax, twice that for the sum of two.
+// The same for a group's score, of experts whose scores are at most `most` in
+// magnitude: p share is at most 5.1 for a sigmoid and 51 for a softmax, twice
+// that for the sum of two, whose terms and whose sum round once each (the two
+// terms may cancel, so their size counts and not the sum's).
 template <bool SIGMOID>
-__device__ __forceinline__ float group_error(float g)
+__device__ __forceinline__ float group_error(float most)
 {
-    return (SIGMOID ? 12.f : 104.f) * kU + 4.f * fabsf(g) * kU;
+    return (SIGMOID ? 12.f : 104.f) * kU + 6.f * most * kU;
 }
 
 __device__ __forceinline__ float key_value(uint32_t k)
@@ -179,7 +181,7 @@ __device__ __forceinline__ uint32_t group_key(uint32_t k1, uint32_t k2, bool top
 // lies above the best one left (infinite where that does not matter).
 template <int NSLOT, int VEC, int TPW>
 __device__ __forceinline__ float keep_groups(uint32_t (&key)[NSLOT], int32_t E, int32_t n_groups, int32_t topk_groups,
-                                             bool top2, float &taken)
+                                             bool top2)
 {
     using G = Group<TPW>;
     constexpr int HW = G::HW;
@@ -237,8 +239,7 @@ __device__ __forceinline__ float keep_groups(uint32_t (&key)[NSLOT], int32_t E, 
 #pragma unroll
     for (int i = 0; i < NSLOT; ++i)
         key[i] = ((chosen >> (gid[i] & 63)) & 1ull) ? key[i] : 0u;
-    taken = key_value(last);
-    return rest <= 1u ? INFINITY : taken - key_value(rest);
+    return rest <= 1u ? INFINITY : key_value(last) - key_value(rest);
 }
 
 // The k + 1 largest of a wave's keys, ties to the smaller id, for one token per
@@ -522,9 +523,12 @@ __global__ __launch_bounds__(kRouteThreads, 8) void route_scored_kernel(ScoredAr
         key[i] = valid && (int32_t)slot_id<VEC, HW>(i, gl) < a.E ? score_key(l[i] + 0.0f) : 0u;
     bool near = false;  // the float32 order is not certain
     if (grouped) {
-        float taken;
-        const float gap = keep_groups<NSLOT, VEC, TPW>(key, a.E, a.n_groups, a.topk_groups, a.top2, taken);
-        near = by_score && gap <= 2.f * group_error<SIGMOID>(taken);
+        float most = 0.f;  // the largest score's magnitude; masked ones do not count
+#pragma unroll
+        for (int i = 0; i < NSLOT; ++i)
+            most = fmaxf(most, key[i] && l[i] != -INFINITY ? fabsf(l[i]) : 0.f);
+        const float gap = keep_groups<NSLOT, VEC, TPW>(key, a.E, a.n_groups, a.topk_groups, a.top2);
+        near = by_score && gap <= 2.f * group_error<SIGMOID>(G::max_f32(most));
         if (by_score && !a.bias) {
             // groups by their scores, experts within them by their logits
             load_row<BF16, NSLOT, VEC, HW>(row, a.E, gl, valid, l);

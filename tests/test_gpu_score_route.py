@@ -110,6 +110,24 @@ def test_close_scores(moe, E, k, G, M, kind):
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,M", [(64, 8, 4), (256, 8, 3), (96, 6, 2), (24, 4, 2)])
+def test_group_sums_that_cancel(moe, E, G, M, kind):
+    """Groups ranked by two scores that nearly cancel (biases of +-40): the sums lie closer than the terms'
+    float32 rounding, 2^-19."""
+    rng = np.random.default_rng(E)
+    l = rng.standard_normal((1, E)).astype(np.float32)
+    p, size = ref.scores(l, kind)[0], E // G
+    b = np.full(E, -100.0, np.float32)
+    first, second = np.arange(G) * size, np.arange(G) * size + 1
+    b[second] = -40.0
+    b[first] = (40.75 - p[first] - p[second]).astype(np.float32)
+    l = l.repeat(50, 0)
+    l[1:, first] += rng.standard_normal((49, G)).astype(np.float32) * 1e-5
+    say(E, G, M, kind)
+    check(moe, torch.from_numpy(l), b, 2, G, M, kind, True, True)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E,G,M", [(64, 1, 1), (256, 8, 4), (510, 1, 1), (768, 16, 3)])
 def test_ties(moe, E, G, M, kind):
     """Few distinct logits and equal biases: exact ties go to the lower id and the lower group."""
