@@ -510,9 +510,17 @@ def _need(t, name: str, ndim: int):
 _HERE = contextlib.nullcontext()
 
 
-def _on(device):
-    """Makes `device` current for the launch: kernels run on their tensors' GPU."""
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _on(device, stream):
+    """Makes `device`, and `stream` where one is given, current: kernels run on
+    their tensors' GPU, and what is allocated for a launch belongs to the
+    launch's stream (memory of another stream could still be in use there, or
+    be handed out again there before the launch is done)."""
+    if stream is None:
+        return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):  # a raw handle, or an object that has one
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _score_flags(logits: torch.Tensor, scores: str, normalize: bool) -> int:
@@ -534,15 +542,15 @@ def moe_route_scored(logits: torch.Tensor, bias: Optional[torch.Tensor], k: int,
     T, E = _need(logits, "logits", 2).shape
     dev = logits.device
     flags = _score_flags(logits, scores, normalize) | (MOE_GROUP_TOP2 if group_top2 else 0)
-    if topk_idx is None:
-        topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
-    if topk_w is None:
-        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    with _on(dev):
+    with _on(dev, stream):
+        if topk_idx is None:
+            topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        if topk_w is None:
+            topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
         _check("moe_route_scored", lib.moe_route_scored(
             _ptr(logits, _LOGITS, "logits", 2), _shaped(bias, "bias", (E,), _F32, dev), T, E, k, n_groups,
             topk_groups, scale, flags, _shaped(topk_idx, "topk_idx", (T, k), _I32, dev),
-            _shaped(topk_w, "topk_w", (T, k), _F32, dev), _stream(stream)))
+            _shaped(topk_w, "topk_w", (T, k), _F32, dev), _stream(None)))
     return topk_idx, topk_w
 
 
@@ -554,13 +562,13 @@ def moe_route_scored_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad
     T, E = _need(logits, "logits", 2).shape
     dev = logits.device
     k = _need(topk_idx, "topk_idx", 2).shape[1]
-    if grad_logits is None:
-        grad_logits = torch.empty_like(logits, memory_format=torch.contiguous_format)
-    with _on(dev):
+    with _on(dev, stream):
+        if grad_logits is None:
+            grad_logits = torch.empty_like(logits, memory_format=torch.contiguous_format)
         _check("moe_route_scored_backward", lib.moe_route_scored_backward(
             _ptr(logits, _LOGITS, "logits", 2), _shaped(topk_idx, "topk_idx", (T, k), _I32, dev),
             _shaped(grad_w, "grad_w", (T, k), _F32, dev), T, E, k, scale, _score_flags(logits, scores, normalize),
-            _shaped(grad_logits, "grad_logits", (T, E), (logits.dtype,), dev), _stream(stream)))
+            _shaped(grad_logits, "grad_logits", (T, E), (logits.dtype,), dev), _stream(None)))
     return grad_logits
 
 
@@ -585,18 +593,18 @@ def moe_combine_backward(grad_out: torch.Tensor, y: Optional[torch.Tensor], pos:
         raise ValueError("grad_w needs y")
     if need_y and topk_w is None:
         raise ValueError("grad_y needs topk_w")
-    if need_y and grad_y is None:
-        grad_y = torch.empty((y_rows, H), dtype=torch.bfloat16, device=dev)
-    if need_w and grad_w is None:
-        grad_w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    grad_y, grad_w = grad_y if need_y else None, grad_w if need_w else None
     fp32 = grad_out.dtype == torch.float32
-    with _on(dev):
+    with _on(dev, stream):
+        if need_y and grad_y is None:
+            grad_y = torch.empty((y_rows, H), dtype=torch.bfloat16, device=dev)
+        if need_w and grad_w is None:
+            grad_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        grad_y, grad_w = grad_y if need_y else None, grad_w if need_w else None
         _check("moe_combine_backward", lib.moe_combine_backward(
             _ptr(grad_out, _F32 if fp32 else _BF16, "grad_out", 2), _shaped(y, "y", (y_rows, H), _BF16, dev), y_rows,
             _shaped(pos, "pos", (T, k), _I32, dev), _shaped(topk_w, "topk_w", (T, k), _F32, dev), T, H, k,
             MOE_COMBINE_OUT_FP32 if fp32 else 0, _shaped(grad_y, "grad_y", (y_rows, H), _BF16, dev),
-            _shaped(grad_w, "grad_w", (T, k), _F32, dev), _stream(stream)))
+            _shaped(grad_w, "grad_w", (T, k), _F32, dev), _stream(None)))
     return grad_y, grad_w
 
 
@@ -621,15 +629,15 @@ def moe_expert_product(x: torch.Tensor, expert_offsets: torch.Tensor, W: torch.T
     if gated and wide % 2:
         raise ValueError("a gated W holds gate and up outputs in equal number")
     O = wide // 2 if gated else wide
-    if y is None:
-        y = torch.empty((max_rows, O), dtype=torch.bfloat16, device=dev)
-    with _on(dev):
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty((max_rows, O), dtype=torch.bfloat16, device=dev)
         _check("moe_expert_product", lib.moe_expert_product(
             _ptr(x, _BF16, "x", 2), _shaped(expert_offsets, "expert_offsets", (El + 1,), _I32, dev), El, max_rows, H,
             O, _shaped(W, "W", (El, wide, H), _BF16, dev), _shaped(bias, "bias", (El, wide), _BF16, dev),
             _shaped(residual, "residual", (max_rows, O), _BF16, dev), _act(act), MOE_PRODUCT_GATED if gated else 0,
             _shaped(pre, "pre", (max_rows, wide), _BF16, dev), _shaped(y, "y", (max_rows, O), _BF16, dev),
-            _stream(stream)))
+            _stream(None)))
     return y
 
 
@@ -643,14 +651,14 @@ def moe_expert_product_dgrad(grad_y: torch.Tensor, expert_offsets: torch.Tensor,
     dev = grad_y.device
     El, _, H = _need(W, "W", 3).shape
     wide = 2 * H if gated else H
-    if grad_x is None:
-        grad_x = torch.empty((max_rows, wide), dtype=torch.bfloat16, device=dev)
-    with _on(dev):
+    with _on(dev, stream):
+        if grad_x is None:
+            grad_x = torch.empty((max_rows, wide), dtype=torch.bfloat16, device=dev)
         _check("moe_expert_product_dgrad", lib.moe_expert_product_dgrad(
             _ptr(grad_y, _BF16, "grad_y", 2), _shaped(expert_offsets, "expert_offsets", (El + 1,), _I32, dev), El,
             max_rows, O, H, _shaped(W, "W", (El, O, H), _BF16, dev), _shaped(pre, "pre", (max_rows, wide), _BF16, dev),
             _act(act), MOE_PRODUCT_GATED if gated else 0, _shaped(grad_x, "grad_x", (max_rows, wide), _BF16, dev),
-            _stream(stream)))
+            _stream(None)))
     return grad_x
 
 
@@ -672,20 +680,20 @@ def moe_expert_product_wgrad(grad_y: torch.Tensor, x: torch.Tensor, expert_offse
     dev = grad_y.device
     H = _need(x, "x", 2).shape[1]
     El = _need(expert_offsets, "expert_offsets", 1).shape[0] - 1
-    if grad_W is None:
-        if accumulate:
-            raise ValueError("accumulate needs grad_W")
-        grad_W = torch.empty((El, O, H), dtype=torch.bfloat16, device=dev)
-    fp32 = grad_W.dtype == torch.float32
+    if grad_W is None and accumulate:
+        raise ValueError("accumulate needs grad_W")
     need = moe_expert_product_wgrad_workspace_size(El, max_rows, O, H)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    with _on(dev):
+    with _on(dev, stream):
+        if grad_W is None:
+            grad_W = torch.empty((El, O, H), dtype=torch.bfloat16, device=dev)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        fp32 = grad_W.dtype == torch.float32
         _check("moe_expert_product_wgrad", lib.moe_expert_product_wgrad(
             _ptr(grad_y, _BF16, "grad_y", 2), _shaped(x, "x", (max_rows, H), _BF16, dev),
             _shaped(expert_offsets, "expert_offsets", (El + 1,), _I32, dev), El, max_rows, O, H,
             (MOE_GRAD_FP32 if fp32 else 0) | (MOE_GRAD_ACCUMULATE if accumulate else 0),
             _shaped(grad_W, "grad_W", (El, O, H), _F32 if fp32 else _BF16, dev),
             _shaped(grad_bias, "grad_bias", (El, O), _F32, dev), _ptr(workspace, (torch.uint8,), "workspace"),
-            0 if workspace is None else workspace.numel(), _stream(stream)))
+            0 if workspace is None else workspace.numel(), _stream(None)))
     return grad_W

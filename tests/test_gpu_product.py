@@ -314,3 +314,26 @@ def test_stream_and_graph(moe):
             step()
             torch.cuda.synchronize()
             want = [t.clone() for t in (y, gx, gW, gb)]
+
+
+def test_workspace_belongs_to_the_launch_s_stream(moe):
+    """The current stream is held up with a write to memory that it has already given back: a workspace or an
+    output for another stream's launch may not be that memory."""
+    rng = np.random.default_rng(8)
+    rows, O, H = 6000, 256, 512
+    gy, x, off = bf16(rng, rows, O), bf16(rng, rows, H), torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    n = moe.moe_expert_product_wgrad_workspace_size(1, rows, O, H)
+    assert n > 0
+    g, v = up(gy), up(x)
+    want = moe.moe_expert_product_wgrad(g, v, off)
+    torch.cuda.synchronize()
+    say("workspace", n)
+    for side in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        blocks = [torch.empty(n, dtype=torch.uint8, device=DEV) for _ in range(3)]
+        torch.cuda._sleep(20_000_000)
+        for b in blocks:
+            b.fill_(255)
+        del b, blocks
+        got = moe.moe_expert_product_wgrad(g, v, off, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
