@@ -146,27 +146,23 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_kernel(ProductArgs p)
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kGemmLdsBytes];
     __shared__ int32_t first[kMaxLocalExperts + 1];
     const int32_t row_tiles = plan_row_tiles<kGemmThreads, kTile>(p.off, p.El, p.max_rows, first);
-    const int64_t nct = (p.N + kCols - 1) / kCols;
+    const uint32_t nct = (uint32_t)(p.N + kCols - 1) / kCols;
     const int64_t wide = PAIR ? 2 * (int64_t)p.N : p.N;
     const int nk = (p.K + kTileK - 1) / kTileK;
     Gemm<false, GRAD> gemm;
     gemm.init_lane();
     // each XCD (blockIdx % 8) takes runs of consecutive tiles
-    const int32_t per_xcd = gridDim.x / 8;
-    const int64_t slot = gridDim.x % 8 ? blockIdx.x : (int64_t)(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
+    const uint32_t slot = gridDim.x % 8 ? blockIdx.x : blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
     // A last round that would leave half the blocks or more idle takes its
     // tiles in two or four slices of rows, one for each block.
-    const int64_t tiles = row_tiles * nct, rest = tiles % gridDim.x, whole = tiles - rest;
-    const int32_t slices = rest * 4 <= gridDim.x ? 4 : (rest * 2 <= gridDim.x ? 2 : 1);
-    for (int64_t u = slot; u < whole + rest * slices; u += gridDim.x) {
-        const int64_t tile = u < whole ? u : whole + (u - whole) / slices;
+    const uint32_t tiles = row_tiles * nct, rest = tiles % gridDim.x, whole = tiles - rest;
+    const uint32_t slices = rest * 4 <= gridDim.x ? 4 : (rest * 2 <= gridDim.x ? 2 : 1);
+    for (uint32_t u = slot; u < whole + rest * slices; u += gridDim.x) {
+        const uint32_t tile = u < whole ? u : whole + (u - whole) / slices;
         const int32_t slice = u < whole ? 0 : (int32_t)((u - whole) % slices);
-        const int32_t most = u < whole ? kTile : kTile / slices;
-        // the same in every lane; saying so keeps the buffer descriptors in scalar
-        // registers (the quotient's vector arithmetic would put a loop around
-        // every load)
-        const int32_t rt = __builtin_amdgcn_readfirstlane((int32_t)(tile / nct));
-        const int32_t n0 = __builtin_amdgcn_readfirstlane((int32_t)(tile % nct)) * kCols;
+        const int32_t most = u < whole ? kTile : kTile / (int32_t)slices;
+        const TileAt which = tile_at(tile, row_tiles, nct);
+        const int32_t rt = which.row, n0 = which.col * kCols;
         const int32_t l = __builtin_amdgcn_readfirstlane(tile_expert(first, p.El, rt));
         const Rows r = expert_rows(p.off, l, p.max_rows);
         const int64_t at = r.begin + (int64_t)(rt - first[l]) * kTile + slice * most;

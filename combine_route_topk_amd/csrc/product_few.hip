@@ -140,8 +140,8 @@ __global__ __launch_bounds__(kFewThreads, 4) void product_few_kernel(ProductArgs
     __shared__ int32_t first[kMaxLocalExperts + 1];
     __shared__ f32x4 part[kFewWaves][2 * NG][kWave];
     const int32_t row_tiles = plan_row_tiles<kFewThreads, kFewRows>(p.off, p.El, p.max_rows, first);
-    const int64_t nct = (p.N + kFewCols - 1) / kFewCols;
-    for (int64_t u = blockIdx.x; u < row_tiles * nct; u += gridDim.x) {
+    const uint32_t nct = (uint32_t)(p.N + kFewCols - 1) / kFewCols;
+    for (uint32_t u = blockIdx.x; u < row_tiles * nct; u += gridDim.x) {
         const int32_t rt = __builtin_amdgcn_readfirstlane((int32_t)(u / nct));
         const int32_t n0 = __builtin_amdgcn_readfirstlane((int32_t)(u % nct)) * kFewCols;
         const int32_t l = __builtin_amdgcn_readfirstlane(tile_expert(first, p.El, rt));

@@ -147,8 +147,8 @@ __global__ __launch_bounds__(kGemmThreads, 2) void wgrad_kernel(WgradArgs p)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kGemmLdsBytes];
     __shared__ uint16_t by_rows[kMaxLocalExperts];  // experts, most rows first
-    const int64_t nh = (p.H + kTile - 1) / kTile, tp = ((p.O + kTile - 1) / kTile) * nh;
-    const int64_t units = p.El * (SPLIT ? p.S : 1) * tp;
+    const uint32_t nh = (uint32_t)(p.H + kTile - 1) / kTile, no = (uint32_t)(p.O + kTile - 1) / kTile, tp = no * nh;
+    const uint32_t units = p.El * (SPLIT ? p.S : 1) * tp;
     const bool sorted = units > gridDim.x;
     if (sorted) {
         // rank by counting, from row counts staged where the tiles will lie
@@ -169,25 +169,25 @@ __global__ __launch_bounds__(kGemmThreads, 2) void wgrad_kernel(WgradArgs p)
     }
     Gemm<true, true> gemm;
     gemm.init_lane();
-    const int32_t per_xcd = gridDim.x / 8;
-    const int64_t slot = gridDim.x % 8 ? blockIdx.x : (int64_t)(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
+    const uint32_t slot = gridDim.x % 8 ? blockIdx.x : blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
     // One unit: a tile's piece s of expert l's rows.
     struct Unit {
-        int64_t tile;
+        uint32_t tile;
         int32_t l, s, o0, h0, nk;
     } next = {0, 0, 0, 0, 0, 0};
-    int64_t round = 0;
+    uint32_t round = 0;
     // Finds this block's next unit, points the operands at it and starts its
     // first loads; false when there is none.
     auto begin = [&]() -> bool {
         for (; round * gridDim.x < units; ++round) {
-            const int64_t u = round * gridDim.x + (round & 1 ? gridDim.x - 1 - slot : slot);
+            const uint32_t u = round * gridDim.x + (round & 1 ? gridDim.x - 1 - slot : slot);
             if (u >= units)
                 continue;
-            const int64_t piece = u / tp;
-            next.tile = u % tp;
-            next.h0 = __builtin_amdgcn_readfirstlane((int32_t)(next.tile % nh)) * kTile;
-            next.o0 = __builtin_amdgcn_readfirstlane((int32_t)(next.tile / nh)) * kTile;
+            const uint32_t piece = u / tp;
+            next.tile = u - piece * tp;
+            const TileAt which = tile_at(next.tile, no, nh);
+            next.o0 = which.row * kTile;
+            next.h0 = which.col * kTile;
             const int32_t e = (int32_t)(SPLIT ? piece / p.S : piece);
             next.s = SPLIT ? __builtin_amdgcn_readfirstlane((int32_t)(piece % p.S)) : 0;
             next.l = __builtin_amdgcn_readfirstlane(sorted ? by_rows[e] : e);
@@ -238,11 +238,11 @@ __global__ __launch_bounds__(kGemmThreads, 2) void wgrad_kernel(WgradArgs p)
 template <bool FP32, bool ACCUMULATE>
 __global__ __launch_bounds__(kGemmThreads, 2) void join_kernel(WgradArgs p)
 {
-    const int64_t nh = (p.H + kTile - 1) / kTile, tp = ((p.O + kTile - 1) / kTile) * nh;
+    const uint32_t nh = (uint32_t)(p.H + kTile - 1) / kTile, no = (uint32_t)(p.O + kTile - 1) / kTile, tp = no * nh;
     Gemm<true, true> gemm;
     gemm.init_lane();
     const int32_t l = (int32_t)(blockIdx.x / tp);
-    const int64_t tile = blockIdx.x % tp;
+    const uint32_t tile = blockIdx.x % tp;
     const Rows r = expert_rows(p.off, l, p.max_rows);
     const int64_t all = ((int64_t)r.end - r.begin + kTileK - 1) / kTileK;
     Acc acc;
@@ -258,9 +258,10 @@ __global__ __launch_bounds__(kGemmThreads, 2) void join_kernel(WgradArgs p)
             acc[i >> 4][(i >> 3) & 1][(i >> 1) & 3][i & 1] +=
                 __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(q + frag_at(i, gemm.wave, gemm.lane)));
     }
-    const int32_t o0 = (int32_t)(tile / nh) * kTile;
-    write_tile<FP32, ACCUMULATE>(p, gemm, acc, l, o0, (int32_t)(tile % nh) * kTile);
-    if (!p.gb || tile % nh != 0 || threadIdx.x >= kTile || o0 + (int32_t)threadIdx.x >= p.O)
+    const TileAt which = tile_at(tile, no, nh);
+    const int32_t o0 = which.row * kTile;
+    write_tile<FP32, ACCUMULATE>(p, gemm, acc, l, o0, which.col * kTile);
+    if (!p.gb || which.col != 0 || threadIdx.x >= kTile || o0 + (int32_t)threadIdx.x >= p.O)
         return;
     const int32_t o = o0 + threadIdx.x;
     float b = 0.f;
