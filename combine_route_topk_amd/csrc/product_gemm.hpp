@@ -40,7 +40,6 @@ constexpr int kGemmBufferFlags = 0x00020000;   // raw byte-addressed buffer
 constexpr uint32_t kOutside = 0x80000000u;     // an offset past every descriptor's end
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 

@@ -112,7 +112,7 @@ __device__ __forceinline__ float score(float l, const Norm &n, float b)
 template <bool SIGMOID>
 __device__ __forceinline__ float score_error(float l, float p, float s, const Norm &n)
 {
-    const float share = SIGMOID ? (1.f - p) * (2.5f * fabsf(l) + 2.f) + 4.f : 2.5f * fabsf(l - n.m) + 50.f;
+    const float share = SIGMOID ? (1.f - p) * (2.5f * fminf(fabsf(l), 1e4f) + 2.f) + 4.f : 2.5f * fabsf(l - n.m) + 50.f;
     return (p * share + fabsf(s)) * kU + 2.3509887e-38f;
 }
 // The same for a group's score, of experts whose scores are at most `most` in
@@ -437,9 +437,17 @@ __device__ __noinline__ int rank_exactly(const void *row, const float *__restric
             mine = lane == g ? kOut : mine;
         }
 #pragma unroll
-        for (int i = 0; i < NS; ++i)
-            if (i * kWave + lane < E && !((chosen >> ((i * kWave + lane) / gsize)) & 1ull))
+        for (int i = 0; i < NS; ++i) {
+            const int32_t e = i * kWave + lane;
+            if (e >= E)
+                continue;
+            if (!((chosen >> (e / gsize)) & 1ull)) {
                 s[i] = kOut;
+            } else if (!bias) {  // the logits' order, also where their scores are the same in 64 bits
+                const double l = load_logit<BF16>(row, e);
+                s[i] = l != l ? kNaNRank : (l == -INFINITY ? kMasked : l);
+            }
+        }
     }
     int id = 0;
     for (int j = 0; j < k; ++j) {
@@ -557,7 +565,7 @@ __global__ __launch_bounds__(kRouteThreads, 8) void route_scored_kernel(ScoredAr
         }
         const float p = score<SIGMOID>(my_l, n, 0.f);
         const float s = my_l == -INFINITY ? -INFINITY : score<SIGMOID>(my_l, n, b);
-        const float err = score_error<SIGMOID>(my_l, p, s, n);
+        const float err = my_l == -INFINITY ? 0.f : score_error<SIGMOID>(my_l, p, s, n);
         // the next lane's, across the wave
         constexpr int kShl1 = 0x130;
         const float l2 = __uint_as_float(dpp::mov<kShl1>(__float_as_uint(my_l), 0u));

@@ -173,6 +173,21 @@ def test_extreme_logits(moe, kind):
     assert torch.isfinite(w).all() and abs(float(w.sum()) - 1) < 1e-5
 
 
+@pytest.mark.parametrize("E,k,G,M", [(64, 8, 8, 4), (512, 10, 16, 4), (96, 6, 6, 2)])
+def test_saturated_groups(moe, E, k, G, M):
+    """Logits whose sigmoids are all 1: groups tie, experts go by their logits; then one infinite logit, whose
+    score of exactly 1 is above a saturated one by less than float32 shows."""
+    rng = np.random.default_rng(E)
+    l = np.stack([rng.permutation(np.linspace(40, 80, E)) for _ in range(20)]).astype(np.float32)
+    say(E, k, G, M)
+    check(moe, torch.from_numpy(l), None, k, G, M, "sigmoid", True, True)
+    x = np.full((3, E), -5.0, np.float32)
+    x[0, 3], x[1, 3], x[2, 1] = 25.0, 25.0, np.inf
+    x[0, 7], x[1, 1], x[2, 3] = np.inf, np.inf, 30.0
+    idx = moe.moe_route_scored(torch.from_numpy(x).to(DEV), torch.zeros(E, device=DEV), 2, scores="sigmoid")[0]
+    assert idx[:, 0].tolist() == [7, 1, 1] and idx[:, 1].tolist() == [3, 3, 3]
+
+
 def test_nan_and_infinite(moe):
     """NaN ranks last under sigmoid; under softmax ids stay distinct and in range."""
     l = torch.randn(20, 64, generator=torch.Generator().manual_seed(1))
