@@ -8,8 +8,8 @@
 // and add their sums through LDS, in the waves' order. A lane loads 32
 // consecutive bytes of W and of x for every 64 k: the k of an MFMA's lane are
 // permuted, alike for both operands, so that four lanes read a row's whole
-// 128-byte line. 16 columns make enough blocks for all CUs even when a single
-// token leaves eight experts with a row each.
+// 128-byte line. 32 columns make two blocks per CU where a single token leaves
+// eight experts with a row each and 2048 columns.
 #include "product_gemm.hpp"
 #include "product_epilogue.hpp"
 
