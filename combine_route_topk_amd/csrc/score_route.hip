@@ -6,10 +6,11 @@
 // order-preserving 32-bit keys. Without a bias the scores of both kinds rise
 // with the logit, so the logit itself is the key and the order is exact. With
 // one, keys are float32 scores, each within a derived bound of the exact
-// value; when two neighbours among the k + 1 best (or the last group taken
-// and the best one left) are closer than their bounds, the whole wave ranks
-// that token again in 64-bit arithmetic. Random scores need that for under 1%
-// of tokens, so the float32 pass sets the time.
+// value; when two neighbours among the k best are closer than their bounds, or
+// the last of them and the best one left (the last group taken and the best
+// one left) closer than a bound for every one left, the whole wave ranks that
+// token again in 64-bit arithmetic. Random scores need that for under 1% of
+// tokens, so the float32 pass sets the time.
 //
 // Backward. Scores are recomputed from the logits. The k gradients of a token
 // are scattered into a row of LDS, so that every lane then reads what belongs
@@ -114,6 +115,15 @@ __device__ __forceinline__ float score_error(float l, float p, float s, const No
 {
     const float share = SIGMOID ? (1.f - p) * (2.5f * fminf(fabsf(l), 1e4f) + 2.f) + 4.f : 2.5f * fabsf(l - n.m) + 50.f;
     return (p * share + fabsf(s)) * kU + 2.3509887e-38f;
+}
+// The same for any expert whose score is at most s, as one bound: experts
+// behind the best one left may have far larger errors than that one, where a
+// large p cancels against its bias. p share is at most 4.3 for a sigmoid, and
+// for a softmax largest at the row's maximum, whose p is n.inv.
+template <bool SIGMOID>
+__device__ __forceinline__ float rest_error(float s, const Norm &n)
+{
+    return ((SIGMOID ? 5.f : 51.f * n.inv) + fabsf(s)) * kU + 2.3509887e-38f;
 }
 // The same for a group's score, of experts whose scores are at most `most` in
 // magnitude: p share is at most 5.1 for a sigmoid and 51 for a softmax, twice
@@ -571,14 +581,17 @@ __global__ __launch_bounds__(kRouteThreads, 8) void route_scored_kernel(ScoredAr
         const float l2 = __uint_as_float(dpp::mov<kShl1>(__float_as_uint(my_l), 0u));
         const float b2 = __uint_as_float(dpp::mov<kShl1>(__float_as_uint(b), 0u));
         const float s2 = __uint_as_float(dpp::mov<kShl1>(__float_as_uint(s), __float_as_uint(-INFINITY)));
-        const float err2 = __uint_as_float(dpp::mov<kShl1>(__float_as_uint(err), 0u));
+        float err2 = __uint_as_float(dpp::mov<kShl1>(__float_as_uint(err), 0u));
+        if (gl == a.k - 1)  // the next lane's stands for all that are left (-inf: masked, or none)
+            err2 = s2 == -INFINITY ? 0.f : rest_error<SIGMOID>(s2, n);
         // An equal pair is ranked by its ids, but where it straddles the last
         // place it may hide a third expert next to it. Masked ones (-inf) give
         // NaN here: their order is known.
         near |= mine && (s - s2 <= err + err2) && (gl == a.k - 1 || !(my_l == l2 && b == b2));
         my_l = mine ? my_l : -INFINITY;
-        // the k best score at least the smallest of these, exactly
-        least = my_l == -INFINITY ? -INFINITY : s - err;
+        // The k best score at least the smallest of these, exactly. Twice the
+        // bound, which holds half a step of s, covers the difference's rounding.
+        least = my_l == -INFINITY ? -INFINITY : s - 2.f * err;
     } else if (mine) {
         my_l = load_logit<BF16>(row, (int32_t)my_e);
     }

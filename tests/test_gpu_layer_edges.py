@@ -1,0 +1,83 @@
+"""Edges of the layer's operators on the GPU against float64: scores that
+cancel against their biases, logits of very large magnitude, NaN in saved
+pre-activations, no kept row at all, weights past 2^31 elements.
+
+Bars: ids equal; weights and gradients as derived beside each check, with
+u = 2^-24, half a step of float32. Every test prints the case it runs before
+touching the GPU.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import ops_reference as ref
+from test_gpu_product import assert_rows, bf16, canary, dn, up
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+LOWEST = {t: torch.finfo(t).min for t in (torch.float32, torch.bfloat16)}
+
+
+@pytest.fixture(scope="module")
+def moe():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    import combine_route_topk_amd
+    return combine_route_topk_amd
+
+
+def say(*a):
+    print("[case]", *a, flush=True)
+
+
+def same_ids(moe, l, b, k, G, M, kind, top2):
+    """Ids equal to float64's, whose scores differ by more than 64 bits' rounding."""
+    x = l.double().numpy()
+    got = moe.moe_route_scored(l.to(DEV), torch.from_numpy(b).to(DEV), k, G, M, kind, True, top2)[0].cpu().numpy()
+    want = ref.route(x, b, k, G, M, kind, True, top2)[0]
+    bad = np.flatnonzero((got != want).any(1))
+    assert not len(bad), f"{len(bad)} of {len(x)} rows differ; row {bad[0]}: {got[bad[0]]} against {want[bad[0]]}"
+
+
+def rivals(E, k, kind, low, start, decoy, size):
+    """Rows in which one expert's score cancels against its bias.
+
+    Experts in front of it hold `low` logits, so that their scores are their
+    biases with next to no error: k - 1 well above, then one at 0.001, with
+    `decoy` another 7e-10 below it. The last expert of the group has a score
+    of about 0.9 and a bias that leaves about 0.001 again, with the error of
+    the 0.9. Its logit passes from row to row through consecutive float32
+    values, which moves its exact score through 0.001 in steps of about 2e-8.
+    Under softmax an expert far below by its bias shares the row with it.
+    """
+    l = np.full((64, E), low, np.float32)
+    b = (-2.0 - 0.125 * (np.arange(E) // size)).astype(np.float32)  # later groups far apart, so that they are certain
+    b[:k - 1] = 1.0 + 0.125 * np.arange(k - 1)
+    s0 = np.float32(0.001)
+    b[k - 1] = s0
+    if decoy:
+        b[k] = s0 - np.float32(7e-10)
+    last = size - 1
+    steps = np.arange(-32, 32).astype(np.int32) + np.float32(start).view(np.int32)
+    l[:, last] = steps.view(np.float32)
+    if kind == "softmax":
+        l[:, last - 1], b[last - 1] = 0.0, -10.0
+    p = ref.scores(l[32:33], kind)[0, last]
+    b[last] = np.float32(float(s0) - p)
+    return l, b
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,G,M", [(8, 1, 1, 1), (16, 3, 1, 1), (64, 8, 1, 1), (96, 2, 1, 1), (130, 4, 1, 1),
+                                     (255, 3, 1, 1), (512, 10, 1, 1), (1000, 5, 1, 1), (64, 2, 8, 2), (510, 3, 5, 2)])
+def test_score_that_cancels_behind_the_last_place(moe, E, k, G, M, kind):
+    """The rival of the last place is not the one next to it in float32: two experts with hardly any error hold
+    places k and k + 1, and the third, with an error far larger than the distance between those, is behind them."""
+    for start in (1.3, 2.078628, 2.7):
+        l, b = rivals(E, k, kind, -40.0, start, True, E // G)
+        say(E, k, G, M, kind, start)
+        s = np.sort(ref.scores(l, kind)[:, :E // G] + b[:E // G], 1)[:, -k - 2:]
+        assert np.diff(s, axis=1).min() > 2.0 ** -48
+        same_ids(moe, torch.from_numpy(l), b, k, G, M, kind, G > 1)
