@@ -68,13 +68,14 @@ __device__ __forceinline__ void load_row(const void *row, int32_t E, int gl, boo
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 // A softmax's maximum (0 where the row has no finite logit, so that no
-// difference is NaN), that in the exponent's base, and the reciprocal of its
-// sum (0 for a sum of 0). m2 is rounded, which scales every term of the sum
-// and every score's numerator alike.
+// difference is NaN), and the reciprocal of its sum (0 for a sum of 0).
 struct Norm {
-    float m, m2, inv;
-    // numerator of a softmax's score
-    __device__ __forceinline__ float term(float l) const { return __builtin_amdgcn_exp2f(fmaf(l, kLog2e, -m2)); }
+    float m, inv;
+    // numerator of a softmax's score, 1 for the maximum whatever its magnitude:
+    // l log2 e - m log2 e by fma would leave the rounding of m's product in the
+    // exponent, hundreds of steps for |m| >= 1e10, and infinity near the type's
+    // lowest value
+    __device__ __forceinline__ float term(float l) const { return fast_exp(l - m); }
 };
 template <int TPW, int NSLOT>
 __device__ __forceinline__ Norm softmax_norm(const float (&l)[NSLOT])
@@ -86,7 +87,7 @@ __device__ __forceinline__ Norm softmax_norm(const float (&l)[NSLOT])
         m = fmaxf(m, l[i]);
     m = G::max_f32(m);
     m = m == -INFINITY ? 0.f : m;
-    Norm n = {m, m * kLog2e, 0.f};
+    Norm n = {m, 0.f};
     float z = 0.f;
 #pragma unroll
     for (int i = 0; i < NSLOT; ++i)
@@ -509,7 +510,7 @@ __global__ __launch_bounds__(kRouteThreads, 8) void route_scored_kernel(ScoredAr
 
     float l[NSLOT];
     load_row<BF16, NSLOT, VEC, HW>(row, a.E, gl, valid, l);
-    Norm n = {0.f, 0.f, 0.f};
+    Norm n = {0.f, 0.f};
     const bool grouped = a.n_groups > 0, by_score = a.bias || (grouped && a.top2 && a.E > a.n_groups);
     if (!SIGMOID && (by_score || !a.normalize))
         n = softmax_norm<TPW>(l);
@@ -679,7 +680,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_backward_kernel(Sc
         }
     }
     float l[NSLOT];
-    Norm n = {0.f, 0.f, 0.f};
+    Norm n = {0.f, 0.f};
     if (dense) {
         load_row<BF16, NSLOT, VEC, HW>(row, a.E, gl, valid, l);
         n = softmax_norm<TPW>(l);

@@ -81,3 +81,67 @@ def test_score_that_cancels_behind_the_last_place(moe, E, k, G, M, kind):
         s = np.sort(ref.scores(l, kind)[:, :E // G] + b[:E // G], 1)[:, -k - 2:]
         assert np.diff(s, axis=1).min() > 2.0 ** -48
         same_ids(moe, torch.from_numpy(l), b, k, G, M, kind, G > 1)
+
+
+def large_rows(E, dtype):
+    """Rows of large logits: one value throughout, two values, and values that differ by a few units."""
+    v = [-1e10, -1e12, -1e30, LOWEST[dtype], 1e10, 1e12, 1e30, torch.finfo(dtype).max]
+    l = torch.tensor(v).repeat(3, 1).t().reshape(-1, 1).repeat(1, E)
+    l[1::3, :E // 2] = LOWEST[dtype]        # the other half, or all where that is the value
+    l[2::3, E // 3:] = -torch.inf
+    n = np.random.default_rng(E).integers(0, 8, (4, E))
+    near = torch.from_numpy(n * 2.0 ** -4 + np.array([[2.0 ** 20], [-2.0 ** 20], [2.0 ** 19], [-2.0 ** 18]])).float()
+    if dtype == torch.bfloat16:             # steps of 2 at 2^8
+        near = torch.from_numpy(n * 2.0 + np.array([[2.0 ** 8], [-2.0 ** 9], [2.0 ** 8], [-2.0 ** 9]])).float()
+    l = torch.cat([l, near]).to(dtype)
+    assert torch.equal(l[-4:].float(), near)
+    return l
+
+
+def spread(x):
+    """Largest |l - max of the row| among scores that do not vanish (exp(-110) is below half of float32's smallest)."""
+    d = x.max(1, keepdims=True) - x
+    return np.where(d < 110, d, 0).max()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k,G,M", [(8, 2, 1, 1), (60, 4, 1, 1), (64, 8, 8, 4), (255, 7, 1, 1), (256, 8, 8, 4),
+                                     (512, 10, 1, 1), (1000, 8, 10, 3)])
+def test_softmax_of_large_logits(moe, E, k, G, M, dtype):
+    """A softmax depends on differences of logits only, whatever their magnitude: 1 / E for a row of one value.
+
+    Bar: an exponential is off by its argument's roundings, at most 2.5 A u for differences up to A, and 2 steps;
+    the sum by that, E u and the additions; so |w - v| <= v (E + 8 A + 24) u."""
+    l = large_rows(E, dtype)
+    x = l.double().numpy()
+    b = ((np.random.default_rng(E).permutation(E) - E / 2) * (0.5 / E / E)).astype(np.float32)
+    for bias in (b, None):
+        for normalize in (False, True):
+            for top2 in ((False, True) if G > 1 else (False,)):
+                say(E, k, G, M, dtype, bias is not None, normalize, top2)
+                idx, w = moe.moe_route_scored(l.to(DEV), None if bias is None else torch.from_numpy(bias).to(DEV), k,
+                                              G, M, "softmax", normalize, top2, 2.5)
+                want, v = ref.route(x, bias, k, G, M, "softmax", normalize, top2, 2.5)
+                bad = np.flatnonzero((idx.cpu().numpy() != want).any(1))
+                assert not len(bad), f"rows {bad}: {idx[bad[0]].tolist()} against {want[bad[0]]}"
+                err = np.abs(w.cpu().double().numpy() - v)
+                assert (err <= np.abs(v) * (E + 8 * spread(x) + 24) * U + 2.0 ** -126).all(), err.max()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k", [(8, 2), (60, 4), (256, 8), (383, 7), (512, 10), (1000, 5)])
+def test_softmax_gradient_of_large_logits(moe, E, k, dtype):
+    """The plain softmax's gradient on the same rows. Bar: a score off by (E + 8 A + 24) u of itself, in a product
+    with a difference of gradients whose terms are at most max |g| each; bf16 adds half a step."""
+    l = large_rows(E, dtype)
+    x, rng = l.double().numpy(), np.random.default_rng(k)
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(len(x))]).astype(np.int32)
+    g = rng.standard_normal((len(x), k)).astype(np.float32)
+    say(E, k, dtype)
+    got = moe.moe_route_scored_backward(l.to(DEV), torch.from_numpy(idx).to(DEV), torch.from_numpy(g).to(DEV),
+                                        "softmax", False, 2.5).cpu().double().numpy()
+    want = ref.route_backward(x, idx, g, "softmax", False, 2.5)
+    tol = 2.5 * 2 * np.abs(g).max(1, keepdims=True) * ref.scores(x, "softmax") * (E + 8 * spread(x) + 48) * U + 2.0 ** -126
+    if dtype == torch.bfloat16:
+        tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(want)
+    assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) - tol).max()
