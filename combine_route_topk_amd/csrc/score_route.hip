@@ -111,10 +111,14 @@ __device__ __forceinline__ float score(float l, const Norm &n, float b)
 // sum and reciprocal each by one or two steps; a sigmoid takes (1 - p) of its
 // exponential's share, a softmax's sum at most 43 kU more (its terms' shares
 // weighted by the terms, and up to 23 additions). The last addition rounds s.
+// |x| is bounded where p has long vanished (exp(-104) is below float32's
+// smallest), so that a finite logit in place of a mask gives 0 and not 0 times
+// infinity, which would pass every comparison as certain.
 template <bool SIGMOID>
 __device__ __forceinline__ float score_error(float l, float p, float s, const Norm &n)
 {
-    const float share = SIGMOID ? (1.f - p) * (2.5f * fminf(fabsf(l), 1e4f) + 2.f) + 4.f : 2.5f * fabsf(l - n.m) + 50.f;
+    const float x = fminf(fabsf(SIGMOID ? l : l - n.m), 1e4f);
+    const float share = SIGMOID ? (1.f - p) * (2.5f * x + 2.f) + 4.f : 2.5f * x + 50.f;
     return (p * share + fabsf(s)) * kU + 2.3509887e-38f;
 }
 // The same for any expert whose score is at most s, as one bound: experts

@@ -145,3 +145,26 @@ def test_softmax_gradient_of_large_logits(moe, E, k, dtype):
     if dtype == torch.bfloat16:
         tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(want)
     assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) - tol).max()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(8, 2), (64, 4), (130, 1), (512, 6)])
+def test_lowest_logit_beside_a_close_score(moe, E, k, kind, dtype):
+    """An expert whose finite logit stands for a mask scores its bias exactly; another lies within float32's
+    rounding of it, at the last place and inside the order."""
+    for extra in (0, 1):  # the pair at places k and k + 1, or k - 1 and k
+        if k + extra > E - 3:
+            continue
+        for i in range(12):
+            l, b = rivals(E, k, kind, LOWEST[dtype], 1.3 + 0.125 * i, False, E)
+            l = torch.from_numpy(l[32:33]).to(dtype)
+            last = E - 1
+            p = ref.scores(l.double().numpy(), kind)[0, last]
+            b[last] = np.float32(0.001 - p)
+            # what that bias leaves is a multiple of its own rounding, about 2^-25: set the other expert right beside
+            exact = p + float(b[last])
+            for d in (-2e-9, 2e-9):
+                b[k - 1] = np.float32(exact + d)
+                say(E, k, kind, dtype, extra, i, d)
+                same_ids(moe, l, b, k + extra, 1, 1, kind, False)
