@@ -134,6 +134,9 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kSqrt2OverPi = 0.79788456080286536f;
 constexpr float kGeluCubic = 0.044715f;
 
+// z within [-30, 30]; NaN stays NaN (a minimum and maximum alone would drop it)
+__device__ __forceinline__ float within_30(float z) { return z != z ? z : fminf(fmaxf(z, -30.f), 30.f); }
+
 // with u = sqrt(2 / pi) (z + c z^3), (1 + tanh u) / 2 = sigmoid(2 u)
 __device__ __forceinline__ float gelu_tanh_cdf(float z)
 {
@@ -169,13 +172,13 @@ __device__ __forceinline__ void act_and_grad(float z, float &f, float &df)
         return;
     }
     case kActGelu: {
-        const float b = fminf(fmaxf(z, -30.f), 30.f), cdf = 0.5f * erfcf(-b * kSqrtHalf);
+        const float b = within_30(z), cdf = 0.5f * erfcf(-b * kSqrtHalf);
         f = z * cdf;
         df = cdf + b * __builtin_amdgcn_exp2f(-0.72134752044448170f * b * b) * kInvSqrt2Pi;
         return;
     }
     case kActGeluTanh: {
-        const float b = fminf(fmaxf(z, -30.f), 30.f), p = gelu_tanh_cdf(b);
+        const float b = within_30(z), p = gelu_tanh_cdf(b);
         f = z * p;
         df = p + 2.f * b * p * (1.f - p) * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * b * b);
         return;

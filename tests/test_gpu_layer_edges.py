@@ -168,3 +168,27 @@ def test_lowest_logit_beside_a_close_score(moe, E, k, kind, dtype):
                 b[k - 1] = np.float32(exact + d)
                 say(E, k, kind, dtype, extra, i, d)
                 same_ids(moe, l, b, k + extra, 1, 1, kind, False)
+
+
+@pytest.mark.parametrize("kind", ref.ACTS)
+@pytest.mark.parametrize("gated", [False, True])
+def test_nan_in_the_saved_pre_activations(moe, kind, gated):
+    """A NaN in pre gives NaN in each gradient that depends on it, and changes nothing else."""
+    rng = np.random.default_rng(11)
+    off = torch.tensor([0, 70, 70, 300], dtype=torch.int32, device=DEV)
+    H, wide = 152, 304 if gated else 152
+    gy, W, z = bf16(rng, 300, 64), bf16(rng, 3, 64, H, scale=0.125), bf16(rng, 300, wide)
+    at = np.zeros((300, wide), bool)
+    at[rng.integers(0, 300, 50), rng.integers(0, wide, 50)] = True
+    dirty = z.clone()
+    dirty[torch.from_numpy(at)] = float("nan")
+    say(kind, gated)
+    clean, got = (moe.moe_expert_product_dgrad(up(gy), off, up(W), up(p), kind, gated).cpu() for p in (z, dirty))
+    if not gated:
+        want = at if kind != "none" else np.zeros_like(at)
+    else:  # d u act'(g) depends on u, and on g but for the identity; d act(g) on g
+        g, u = at[:, :H], at[:, H:]
+        want = np.concatenate([u | g if kind != "none" else u, g], 1)
+    assert (np.isnan(got.float().numpy()) == want).all()
+    keep = torch.from_numpy(~want)
+    assert torch.equal(got.view(torch.int16)[keep], clean.view(torch.int16)[keep])
