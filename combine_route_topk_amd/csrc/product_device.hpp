@@ -189,8 +189,5 @@ __device__ __forceinline__ void act_and_grad(float z, float &f, float &df)
     }
 }
 
-__device__ __forceinline__ float bf16_to_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-__device__ __forceinline__ uint16_t f32_to_bf16(float v) { return (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu); }
-
 }  // namespace
 }  // namespace moe
