@@ -600,10 +600,12 @@ def moe_combine_backward(grad_out: torch.Tensor, y: Optional[torch.Tensor], pos:
         if need_w and grad_w is None:
             grad_w = torch.empty((T, k), dtype=torch.float32, device=dev)
         grad_y, grad_w = grad_y if need_y else None, grad_w if need_w else None
+        go, gy = _ptr(grad_out, _F32 if fp32 else _BF16, "grad_out", 2), _shaped(grad_y, "grad_y", (y_rows, H), _BF16, dev)
+        if need_y and y_rows == 0:
+            gy = go  # an empty tensor has no address; with no rows nothing is written through this one
         _check("moe_combine_backward", lib.moe_combine_backward(
-            _ptr(grad_out, _F32 if fp32 else _BF16, "grad_out", 2), _shaped(y, "y", (y_rows, H), _BF16, dev), y_rows,
-            _shaped(pos, "pos", (T, k), _I32, dev), _shaped(topk_w, "topk_w", (T, k), _F32, dev), T, H, k,
-            MOE_COMBINE_OUT_FP32 if fp32 else 0, _shaped(grad_y, "grad_y", (y_rows, H), _BF16, dev),
+            go, _shaped(y, "y", (y_rows, H), _BF16, dev), y_rows, _shaped(pos, "pos", (T, k), _I32, dev),
+            _shaped(topk_w, "topk_w", (T, k), _F32, dev), T, H, k, MOE_COMBINE_OUT_FP32 if fp32 else 0, gy,
             _shaped(grad_w, "grad_w", (T, k), _F32, dev), _stream(None)))
     return grad_y, grad_w
 

@@ -192,3 +192,18 @@ def test_nan_in_the_saved_pre_activations(moe, kind, gated):
     assert (np.isnan(got.float().numpy()) == want).all()
     keep = torch.from_numpy(~want)
     assert torch.equal(got.view(torch.int16)[keep], clean.view(torch.int16)[keep])
+
+
+def test_combine_gradient_without_rows(moe):
+    """No replica was kept: an empty grad_y, alone or with the weights' gradients, which are 0."""
+    g = torch.randn(6, 64, device=DEV).bfloat16()
+    pos, w = torch.full((6, 2), -1, dtype=torch.int32, device=DEV), torch.ones(6, 2, device=DEV)
+    y = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV)
+    for kw in (dict(y=y), dict(y=None, y_rows=0), dict(y=None, grad_y=torch.empty_like(y))):
+        say(sorted(kw))
+        gy, gw = moe.moe_combine_backward(g, pos=pos, topk_w=w, need_w=False, **kw)
+        assert gy.shape == (0, 64) and gy.dtype == torch.bfloat16 and gw is None
+    gy, gw = moe.moe_combine_backward(g, y, pos, w)
+    assert gy.shape == (0, 64) and (gw == 0).all()
+    gy, gw = moe.moe_combine_backward(g, y, pos, None, need_y=False)
+    assert gy is None and (gw == 0).all()
