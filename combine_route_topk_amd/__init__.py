@@ -514,9 +514,12 @@ def _on(device, stream):
     """Makes `device`, and `stream` where one is given, current: kernels run on
     their tensors' GPU, and what is allocated for a launch belongs to the
     launch's stream (memory of another stream could still be in use there, or
-    be handed out again there before the launch is done)."""
+    be handed out again there before the launch is done). A stream of another
+    GPU is refused; a raw handle does not say which GPU it is of."""
     if stream is None:
         return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if getattr(stream, "device", device) != device:
+        raise ValueError(f"stream is on {stream.device}, arguments on {device}")
     if not isinstance(stream, torch.cuda.Stream):  # a raw handle, or an object that has one
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
         stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
