@@ -680,7 +680,7 @@ def moe_expert_product_wgrad(grad_y: torch.Tensor, x: torch.Tensor, expert_offse
                              stream=None) -> torch.Tensor:
     """grad_W [E_l, O, H] (bf16 when allocated here; float32 when given so) and,
     when given, grad_bias [E_l, O] float32 (see moe_expert_product_wgrad).
-    accumulate adds to both, which must then be given, grad_W in float32."""
+    accumulate adds to them; grad_W must then be given, in float32."""
     max_rows, O = _need(grad_y, "grad_y", 2).shape
     dev = grad_y.device
     H = _need(x, "x", 2).shape[1]
@@ -699,6 +699,7 @@ def moe_expert_product_wgrad(grad_y: torch.Tensor, x: torch.Tensor, expert_offse
             _shaped(expert_offsets, "expert_offsets", (El + 1,), _I32, dev), El, max_rows, O, H,
             (MOE_GRAD_FP32 if fp32 else 0) | (MOE_GRAD_ACCUMULATE if accumulate else 0),
             _shaped(grad_W, "grad_W", (El, O, H), _F32 if fp32 else _BF16, dev),
-            _shaped(grad_bias, "grad_bias", (El, O), _F32, dev), _ptr(workspace, (torch.uint8,), "workspace"),
+            _shaped(grad_bias, "grad_bias", (El, O), _F32, dev),
+            None if workspace is None else _shaped(workspace, "workspace", workspace.shape, (torch.uint8,), dev),
             0 if workspace is None else workspace.numel(), _stream(None)))
     return grad_W

@@ -79,3 +79,12 @@ def test_stream_of_another_device(moe, monkeypatch):
     for call in calls(moe, stream=Stream()):
         with pytest.raises(ValueError, match="stream is on cuda:1"):
             call()
+
+
+def test_workspace_of_another_device(moe, monkeypatch):
+    monkeypatch.setattr(moe, "_stream", lambda s: 0)
+    y, x, off, V = Tensor((4, 16), BF), Tensor((4, 8), BF), Tensor((3,), I), Tensor((2, 16, 8), F)
+    with pytest.raises(ValueError, match="workspace is on cuda:1"):
+        moe.moe_expert_product_wgrad(y, x, off, V, workspace=Tensor((4096,), torch.uint8, 1))
+    with pytest.raises(AssertionError, match="the library was called"):
+        moe.moe_expert_product_wgrad(y, x, off, V, workspace=Tensor((4096,), torch.uint8))
