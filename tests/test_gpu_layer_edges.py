@@ -207,3 +207,28 @@ def test_combine_gradient_without_rows(moe):
     assert gy.shape == (0, 64) and (gw == 0).all()
     gy, gw = moe.moe_combine_backward(g, y, pos, None, need_y=False)
     assert gy is None and (gw == 0).all()
+
+
+def test_weights_past_32_bit_offsets(moe):
+    """33 experts of 2^26 weights each; the last, behind 2^31 elements, holds values of its own and has all rows.
+    Few rows take the kernel that reads W straight into fragments (at most 16 rows for each of the 33 experts on
+    average, 2048 columns of x), more take the tiles; the input gradient reads W along its other axis."""
+    El, O, H = 33, 32768, 2048
+    rng = np.random.default_rng(12)
+    W = torch.full((El, O, H), 0.5, dtype=torch.bfloat16, device=DEV)
+    last = bf16(rng, 1, O, H, scale=H ** -0.5)
+    W[-1] = last[0].to(DEV)
+    V = dn(last)
+    for rows in (20, 600):
+        off = torch.zeros(El + 1, dtype=torch.int32, device=DEV)
+        off[-1] = rows
+        x, gy = bf16(rng, rows, H), bf16(rng, rows, O, scale=0.125)
+        say(El, O, H, rows)
+        for gated in (False, True):
+            y = canary(rows, O // 2 if gated else O)
+            moe.moe_expert_product(up(x), off, W, act="silu", gated=gated, y=y)
+            wy, _, _, ey = ref.product(dn(x[:20]), [0, 20], V, None, None, "silu", gated)
+            assert_rows(y[:20], wy, ey, 20, "y")
+        g = canary(rows, H)
+        moe.moe_expert_product_dgrad(up(gy), off, W, grad_x=g)
+        assert_rows(g[:20], *ref.dgrad(dn(gy[:20]), [0, 20], V), 20, "grad_x")
