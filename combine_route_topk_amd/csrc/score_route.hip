@@ -10,7 +10,8 @@
 // the last of them and the best one left (the last group taken and the best
 // one left) closer than a bound for every one left, the whole wave ranks that
 // token again in 64-bit arithmetic. Random scores need that for under 1% of
-// tokens, so the float32 pass sets the time.
+// tokens, so the float32 pass sets the time. Rows of more than 512 experts are
+// ranked in 64 bits from the start.
 //
 // Backward. Scores are recomputed from the logits. The k gradients of a token
 // are scattered into a row of LDS, so that every lane then reads what belongs
@@ -351,12 +352,14 @@ struct Candidates {
     double s[kWave];
     int32_t e[kWave];
 };
-template <int NS, bool BF16, bool SIGMOID>
-__device__ __noinline__ int rank_exactly(const void *row, const float *__restrict__ bias, int32_t E, int32_t k,
-                                         int32_t n_groups, int32_t topk_groups, bool top2, float least,
-                                         Candidates *__restrict__ cand)
+// !FEW: every expert takes part in the rounds, and without a bias the logits
+// are ranked (their scores only where groups go by the sum of two).
+template <int NS, bool BF16, bool SIGMOID, bool FEW>
+__device__ int rank_exactly(const void *row, const float *__restrict__ bias, int32_t E, int32_t k, int32_t n_groups,
+                            int32_t topk_groups, bool top2, float least, Candidates *__restrict__ cand)
 {
     const int lane = threadIdx.x & (kWave - 1);
+    const bool by_logit = !FEW && !bias && !(n_groups > 0 && top2);
     double s[NS], m = -INFINITY, z = 0.;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
@@ -369,7 +372,7 @@ __device__ __noinline__ int rank_exactly(const void *row, const float *__restric
         m = m == -INFINITY ? 0. : m;
     }
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < NS && !by_logit; ++i) {
         const double l = s[i];
         const double u = l == -INFINITY ? 0. : exp(SIGMOID ? -l : l - m);
         if (SIGMOID)
@@ -388,11 +391,11 @@ __device__ __noinline__ int rank_exactly(const void *row, const float *__restric
             continue;
         }
         double v = s[i];
-        if (v != -INFINITY)
+        if (v != -INFINITY && !by_logit)
             v = (SIGMOID ? v : v / z) + (bias ? (double)bias[e] : 0.);
         s[i] = v != v ? kNaNRank : (v == -INFINITY ? kMasked : v);
     }
-    if (n_groups == 0) {
+    if (FEW && n_groups == 0) {
         int n = 0;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
@@ -494,6 +497,30 @@ struct ScoredArgs {
     int32_t *topk_idx;
     float *topk_w;
 };
+
+// The weight of a token's selected expert, before the scale: my_l is its logit
+// in the lanes of `mine`, -inf in the others; n is needed for a softmax that is
+// not normalised.
+template <class G, bool SIGMOID>
+__device__ __forceinline__ float selected_weight(float my_l, bool mine, bool normalize, const Norm &n)
+{
+    if (normalize) {
+        // softmax over the selected; a sigmoid's e^m scales every term alike,
+        // so that scores far below float32's range keep their ratios
+        const float m = G::max_f32(my_l);
+        float u = 0.f;
+        if (SIGMOID)
+            u = my_l > 0.f ? 1.f / (1.f + expf(-my_l)) : expf(my_l - fminf(m, 0.f)) / (1.f + expf(my_l));
+        else
+            u = expf(my_l - m);
+        u = mine && my_l != -INFINITY ? u : 0.f;
+        const float z = G::sum_f32(u);
+        return z == 0.f ? 0.f : u / z;
+    }
+    if (my_l == -INFINITY)
+        return 0.f;
+    return SIGMOID ? 1.f / (1.f + expf(-my_l)) : n.term(my_l) * n.inv;
+}
 
 template <int NSLOT, int VEC, int TPW, bool BF16, bool SIGMOID>
 __global__ __launch_bounds__(kRouteThreads, 8) void route_scored_kernel(ScoredArgs a)
@@ -610,8 +637,11 @@ __global__ __launch_bounds__(kRouteThreads, 8) void route_scored_kernel(ScoredAr
         again &= ~lanes;
         const char *r = static_cast<const char *>(a.logits) + (t0 + base / HW) * row_bytes;
         constexpr int NS = (NSLOT * HW + kWave - 1) / kWave;
-        const int id = rank_exactly<NS, BF16, SIGMOID>(r, a.bias, a.E, a.k, a.n_groups, a.topk_groups, a.top2,
-                                                           __shfl(least, base, kWave), &cand[threadIdx.x / kWave]);
+        const float from = __shfl(least, base, kWave);
+        Candidates *const c = &cand[threadIdx.x / kWave];
+        int id;
+        [[clang::noinline]] id = rank_exactly<NS, BF16, SIGMOID, true>(r, a.bias, a.E, a.k, a.n_groups, a.topk_groups,
+                                                                       a.top2, from, c);
         const int got = __shfl(id, gl, kWave);
         if (gbase == base) {
             my_e = (uint32_t)got;
@@ -619,27 +649,45 @@ __global__ __launch_bounds__(kRouteThreads, 8) void route_scored_kernel(ScoredAr
         }
     }
 
-    float w;
-    if (a.normalize) {
-        // softmax over the selected; a sigmoid's e^m scales every term alike,
-        // so that scores far below float32's range keep their ratios
-        const float m = G::max_f32(my_l);
-        float u = 0.f;
-        if (SIGMOID)
-            u = my_l > 0.f ? 1.f / (1.f + expf(-my_l)) : expf(my_l - fminf(m, 0.f)) / (1.f + expf(my_l));
-        else
-            u = expf(my_l - m);
-        u = mine && my_l != -INFINITY ? u : 0.f;
-        const float z = G::sum_f32(u);
-        w = z == 0.f ? 0.f : u / z;
-    } else if (my_l == -INFINITY) {
-        w = 0.f;
-    } else {
-        w = SIGMOID ? 1.f / (1.f + expf(-my_l)) : n.term(my_l) * n.inv;
-    }
+    const float w = selected_weight<G, SIGMOID>(my_l, mine, a.normalize, n);
     if (mine) {
         a.topk_idx[t * a.k + gl] = (int32_t)my_e;
         a.topk_w[t * a.k + gl] = a.scale * w;
+    }
+}
+
+// More than 512 experts: one wave ranks a token in 64 bits from the start, 16
+// experts a lane, every value in registers at four waves a SIMD: 183 us for
+// 32768 tokens, 1024 experts, k = 8, softmax with a bias; bound by the rounds'
+// reductions over the wave. Float32 keys, 16 a lane at eight waves, took 111 us
+// and spilled up to 63 registers, the row's address among them, to scratch. One
+// such launch ended in a memory fault that the kernel's own accesses do not
+// explain (followed lane by lane, every address is in bounds), so that kernel
+// is not used.
+template <bool BF16, bool SIGMOID>
+__global__ __launch_bounds__(kRouteThreads, 4) void route_scored_wide_kernel(ScoredArgs a)
+{
+    constexpr int kSlots = 16;
+    const int64_t t = (int64_t)blockIdx.x * kWavesPerBlock + threadIdx.x / kWave;
+    if (t >= a.T)
+        return;  // whole waves
+    const int lane = threadIdx.x & (kWave - 1);
+    const char *row = static_cast<const char *>(a.logits) + t * a.E * (BF16 ? 2 : 4);
+    int32_t e;
+    [[clang::always_inline]] e = rank_exactly<kSlots, BF16, SIGMOID, false>(
+        row, a.bias, a.E, a.k, a.n_groups, a.topk_groups, a.top2 && a.E > a.n_groups, -INFINITY, nullptr);
+    Norm n = {0.f, 0.f};
+    if (!SIGMOID && !a.normalize) {
+        float l[kSlots];
+        load_row<BF16, kSlots, 1, kWave>(row, a.E, lane, true, l);
+        n = softmax_norm<1>(l);
+    }
+    const bool mine = lane < a.k;
+    const float my_l = mine ? load_logit<BF16>(row, e) : -INFINITY;
+    const float w = selected_weight<Group<1>, SIGMOID>(my_l, mine, a.normalize, n);
+    if (mine) {
+        a.topk_idx[t * a.k + lane] = e;
+        a.topk_w[t * a.k + lane] = a.scale * w;
     }
 }
 
@@ -785,8 +833,11 @@ hipError_t launch(const ScoredArgs &args, hipStream_t stream)
         a.logits = static_cast<const char *>(a.logits) + t0 * a.E * (BF16 ? 2 : 4);
         a.topk_idx += t0 * a.k;
         a.topk_w += t0 * a.k;
-        hipLaunchKernelGGL((route_scored_kernel<NSLOT, VEC, TPW, BF16, SIGMOID>), grid, dim3(kRouteThreads), 0, stream,
-                           a);
+        if constexpr (NSLOT <= 8)
+            hipLaunchKernelGGL((route_scored_kernel<NSLOT, VEC, TPW, BF16, SIGMOID>), grid, dim3(kRouteThreads), 0,
+                               stream, a);
+        else
+            hipLaunchKernelGGL((route_scored_wide_kernel<BF16, SIGMOID>), grid, dim3(kRouteThreads), 0, stream, a);
     });
 }
 template <int NSLOT, int VEC, int TPW, bool BF16, bool SIGMOID>

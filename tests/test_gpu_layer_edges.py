@@ -100,7 +100,8 @@ def large_rows(E, dtype):
 
 def spread(x):
     """Largest |l - max of the row| among scores that do not vanish (exp(-110) is below half of float32's smallest)."""
-    d = x.max(1, keepdims=True) - x
+    with np.errstate(invalid="ignore"):  # a row of -inf only
+        d = x.max(1, keepdims=True) - x
     return np.where(d < 110, d, 0).max()
 
 
@@ -232,3 +233,32 @@ def test_weights_past_32_bit_offsets(moe):
         g = canary(rows, H)
         moe.moe_expert_product_dgrad(up(gy), off, W, grad_x=g)
         assert_rows(g[:20], *ref.dgrad(dn(gy[:20]), [0, 20], V), 20, "grad_x")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,G,M", [(513, 10, 1, 1), (640, 32, 1, 1), (768, 8, 16, 3), (1000, 6, 8, 4), (1024, 9, 64, 5)])
+def test_more_than_512_experts(moe, E, k, G, M, kind, dtype):
+    """Wide rows have a kernel of their own: with and without a bias, masked rows, saturated logits in order. The
+    weights' bar is that of test_softmax_of_large_logits, with A the largest |logit| for a sigmoid."""
+    rng = np.random.default_rng(E + k)
+    l = torch.from_numpy(rng.standard_normal((300, E)).astype(np.float32)).to(dtype)
+    l[200:250] = torch.where(torch.from_numpy(rng.random((50, E)) < 0.97), torch.tensor(-torch.inf, dtype=dtype), l[200:250])
+    l[250] = -torch.inf
+    l[251:260] = torch.from_numpy(np.stack([rng.permutation(E) * 0.125 + 30 for _ in range(9)])).to(dtype)
+    x = l.double().numpy()
+    A = spread(x[:251]) if kind == "softmax" else np.abs(x[np.isfinite(x)]).max()
+    b = (rng.permutation(E) * (0.2 / E / E)).astype(np.float32)
+    for bias in (b, None):
+        for normalize in (True, False):
+            for top2 in ((False, True) if G > 1 else (False,)):
+                say(E, k, G, M, kind, dtype, bias is not None, normalize, top2)
+                rows = 260 if bias is None and not top2 else 251  # saturated scores are ordered by their logits
+                idx, w = moe.moe_route_scored(l[:rows].to(DEV), None if bias is None else torch.from_numpy(bias).to(DEV),
+                                              k, G, M, kind, normalize, top2, 2.5)
+                want, v = ref.route(x[:rows], bias, k, G, M, kind, normalize, top2, 2.5)
+                bad = np.flatnonzero((idx.cpu().numpy() != want).any(1))
+                assert not len(bad), f"rows {bad}: {idx[bad[0]].tolist()} against {want[bad[0]]}"
+                B = max(A, spread(x[251:])) if kind == "softmax" and rows == 260 else A
+                err = np.abs(w.cpu().double().numpy() - v)
+                assert (err <= np.abs(v) * (E + 8 * B + 24) * U + 2.0 ** -126).all(), err.max()
