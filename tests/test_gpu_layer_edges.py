@@ -262,3 +262,64 @@ def test_more_than_512_experts(moe, E, k, G, M, kind, dtype):
                 B = max(A, spread(x[251:])) if kind == "softmax" and rows == 260 else A
                 err = np.abs(w.cpu().double().numpy() - v)
                 assert (err <= np.abs(v) * (E + 8 * B + 24) * U + 2.0 ** -126).all(), err.max()
+
+
+@pytest.mark.parametrize("rows", [3, 300])
+def test_products_of_the_widest_rows(moe, rows):
+    """H and O at their limit of 65536, one at a time, on both kernels of the product and in the gradients."""
+    rng = np.random.default_rng(rows)
+    off = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    for H, O in ((65536, 16), (16, 65536)):
+        x, gy = bf16(rng, rows, H), bf16(rng, rows, O)
+        for gated in (False, True):
+            W = bf16(rng, 1, 2 * O if gated else O, H, scale=H ** -0.5)
+            say(rows, H, O, gated)
+            y, z = canary(rows, O), canary(rows, 2 * O if gated else O)
+            moe.moe_expert_product(up(x), off, up(W), act="silu", gated=gated, y=y, pre=z)
+            wy, wz, ez, ey = ref.product(dn(x), [0, rows], dn(W), None, None, "silu", gated)
+            assert_rows(y, wy, ey, rows, "y"), assert_rows(z, wz, ez, rows, "pre")
+        V, p = bf16(rng, 1, O, H, scale=O ** -0.5), bf16(rng, rows, 2 * H)
+        g = canary(rows, 2 * H)
+        moe.moe_expert_product_dgrad(up(gy), off, up(V), up(p), "silu", True, g)
+        assert_rows(g, *ref.dgrad(dn(gy), [0, rows], dn(V), dn(p), "silu", True), rows, "grad_x")
+        gW, gb = torch.empty(1, O, H, device=DEV), torch.empty(1, O, device=DEV)
+        moe.moe_expert_product_wgrad(up(gy), up(x), off, gW, gb)
+        vW, vb, eW, eb = ref.wgrad(dn(gy), dn(x), [0, rows], 1)
+        assert (np.abs(gW.cpu().double().numpy() - vW) <= eW + 2.0 ** -126).all()
+        assert (np.abs(gb.cpu().double().numpy() - vb) <= eb + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("T,E,k", [(2 ** 22 + 3, 516, 4), (2 ** 24 + 9, 130, 2)])
+def test_route_of_very_many_tokens(moe, T, E, k):
+    """More than 2^31 logits, and more tokens than one launch takes: rows repeat, so their results do, bit for bit."""
+    R = 1000
+    base = torch.randn(R, E, generator=torch.Generator().manual_seed(E)).bfloat16().to(DEV)
+    b = (torch.rand(E, generator=torch.Generator().manual_seed(k)) * 0.1).to(DEV)
+    at = torch.arange(T, device=DEV) % R
+    say(T, E, k)
+    few = moe.moe_route_scored(base, b, k, scores="sigmoid")
+    l = base[at]
+    idx, w = moe.moe_route_scored(l, b, k, scores="sigmoid")
+    assert torch.equal(idx, few[0][at]) and torch.equal(w, few[1][at])
+    g = torch.randn(R, k, generator=torch.Generator().manual_seed(1)).to(DEV)
+    want = moe.moe_route_scored_backward(base, few[0], g, "softmax", False)
+    got = moe.moe_route_scored_backward(l, idx, g[at], "softmax", False)
+    for t in range(0, T, 2 ** 20):  # in parts, so that no second copy of all of it is held
+        assert torch.equal(got[t:t + 2 ** 20], want[at[t:t + 2 ** 20]])
+
+
+def test_combine_gradient_of_very_many_tokens(moe):
+    """More tokens than one launch takes, of one replica each."""
+    T, H = 2 ** 24 + 5, 8
+    gen = torch.Generator(device=DEV).manual_seed(0)
+    g = torch.randn(T, H, generator=gen, device=DEV).bfloat16()
+    y = torch.randn(T, H, generator=gen, device=DEV).bfloat16()
+    w = torch.randn(T, 1, generator=gen, device=DEV)
+    pos = torch.arange(T - 1, -1, -1, dtype=torch.int32, device=DEV)[:, None]
+    say(T, H)
+    gy, gw = moe.moe_combine_backward(g, y, pos, w)
+    # one product, rounded to float32 and to bf16; a sum of 8 exact products
+    want = (w.double() * g.double()).flip(0)
+    assert ((gy.double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -20) + 2.0 ** -134).all()
+    terms = g.double() * y.double().flip(0)
+    assert ((gw[:, 0].double() - terms.sum(1)).abs() <= 16 * U * terms.abs().sum(1)).all()
