@@ -197,7 +197,9 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_kernel(ProductArgs p)
 
 
 // Whether the kernel for few rows is the faster one, by the average rows of an
-// expert. On MI355X, in us, few against tiles:
+// expert. The host knows max_rows, not the rows there are: a buffer sized for
+// the worst case takes the tiles however few of its rows are used, at the cost
+// that the figures show for few rows. On MI355X, in us, few against tiles:
 //   too few tiles for the CUs: 8 experts, 2048 by 2 x 768: 12 against 27 at 1
 //   row, 16 / 28 at 32, 25 / 28 at 48; 4 experts, 7168 by 7168: 79 / 105 at
 //   1 row, 97 / 107 at 16, 112 / 108 at 24;

@@ -93,9 +93,9 @@ __device__ __forceinline__ int32_t tile_expert(const int32_t *first, int32_t El,
 
 // Row and column of tile t in a rows x cols grid of tiles. Wide grids are
 // walked four rows at a time, so that the 32 consecutive tiles of an XCD are
-// about four by eight and share their operands in its L2: 107 against 113 us
-// for 16 x 28 tiles (4093 x 2048 by 7168), 771 against 815 us for 32 x 32
-// (8192 cubed).
+// about four by eight and share their operands in its L2: 114 against 118 us
+// for 16 x 28 tiles (4093 x 2048 by 7168, bias and residual), 733 against 783 us
+// for 32 x 32 (8192 cubed).
 struct TileAt {
     int32_t row, col;
 };

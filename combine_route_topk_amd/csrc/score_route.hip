@@ -525,7 +525,8 @@ __device__ __forceinline__ float selected_weight(float my_l, bool mine, bool nor
 template <int NSLOT, int VEC, int TPW, bool BF16, bool SIGMOID>
 __global__ __launch_bounds__(kRouteThreads, 8) void route_scored_kernel(ScoredArgs a)
 {
-    // eight waves a SIMD: the 64-bit ranking spills for it, the rest does not
+    // eight waves a SIMD: the 64-bit ranking of eight slots, a function of its
+    // own, saves registers to scratch for it; the kernels spill none
     __shared__ Candidates cand[kWavesPerBlock];
     using G = Group<TPW>;
     constexpr int HW = G::HW;
@@ -660,7 +661,7 @@ __global__ __launch_bounds__(kRouteThreads, 8) void route_scored_kernel(ScoredAr
 // experts a lane, every value in registers at four waves a SIMD: 183 us for
 // 32768 tokens, 1024 experts, k = 8, softmax with a bias; bound by the rounds'
 // reductions over the wave. Float32 keys, 16 a lane at eight waves, took 111 us
-// and spilled up to 63 registers, the row's address among them, to scratch. One
+// and spilled up to 47 registers, the row's address among them, to scratch. One
 // such launch ended in a memory fault that the kernel's own accesses do not
 // explain (followed lane by lane, every address is in bounds), so that kernel
 // is not used.

@@ -670,6 +670,9 @@ typedef enum moe_act {
  * moe_recv_regroup_layout (local_expert_offsets) write them; an expert may
  * have none. Rows from expert_offsets[E_l] on are neither read nor written.
  * An always-active shared expert is E_l = 1 with offsets {0, T}.
+ * Whether the kernel for few rows per expert runs follows from max_rows / E_l,
+ * since the offsets are on the device: for decoding, a max_rows near the rows
+ * there are is up to twice as fast as one for the worst case.
  *
  * Defined by: "MoE All-to-All Dispatch and Ragged Routing", "Why MoE Token
  * Dispatch is All-to-All" (a GPU computes its local experts on the rows it
