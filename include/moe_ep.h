@@ -569,9 +569,10 @@ moe_status_t moe_expert_return_slots(int32_t *slots);
  *     two scores lie closer than float32 resolves, the token is ranked again
  *     in 64 bits).
  *   topk_w[j] = scale * p[e_j] / sum_i p[e_i] with MOE_ROUTE_NORMALIZE, else
- *     scale * p[e_j]; computed in float32. Masked experts, which are selected
- *     only when too few others are left, get 0; a row whose selected scores
- *     are all 0 gets zeros.
+ *     scale * p[e_j]; computed in float32. Normalised weights keep the ratios
+ *     of scores below float32's range. Masked experts, which are selected only
+ *     when too few others are left, get 0; a row whose selected experts are all
+ *     masked gets zeros.
  *   For a row that holds NaN or +inf under softmax, ids are distinct and in
  *     range and nothing else is specified.
  *

@@ -323,3 +323,60 @@ def test_combine_gradient_of_very_many_tokens(moe):
     assert ((gy.double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -20) + 2.0 ** -134).all()
     terms = g.double() * y.double().flip(0)
     assert ((gw[:, 0].double() - terms.sum(1)).abs() <= 16 * U * terms.abs().sum(1)).all()
+
+
+def test_random_close_scores(moe):
+    """Rows whose scores cancel against their biases to a common value within 1e-12 to 1e-4, deep, saturated and
+    masked logits among them: ids equal wherever 64 bits tell the scores apart."""
+    rng, rows = np.random.default_rng(17), 0
+    for i in range(600):
+        G = int(rng.choice([1, 1, 1, 2, 4, 8]))
+        size = int(rng.integers(max(2, 8 // G), 600 // G + 1))
+        E, M = G * size, int(rng.integers(1, G + 1))
+        k = int(rng.integers(1, min(12, M * size) + 1))
+        kind, top2 = ("softmax", "sigmoid")[int(rng.integers(2))], G > 1 and bool(rng.integers(2))
+        x, at = rng.standard_normal(E) * rng.choice([0.3, 1, 4]), rng.random(E)
+        pool = int(rng.integers(5))
+        x = np.where((pool in (1, 2)) & (at < 0.4), -40 + rng.standard_normal(E), x)
+        x = np.where((pool in (2, 3)) & (at > 0.7), LOWEST[torch.float32], x)
+        x = np.where((pool == 4) & (at < 0.5), rng.uniform(5, 25, E), x).astype(np.float32)
+        l, j = x[None].repeat(32, 0), rng.integers(0, E, (32, 3))
+        near = (np.take_along_axis(l, j, 1).view(np.int32) + rng.integers(-40, 40, (32, 3))).astype(np.int32).view(np.float32)
+        np.put_along_axis(l, j, np.where(np.isfinite(near), near, np.take_along_axis(l, j, 1)), 1)
+        target, scale = rng.choice([0.0, 0.001, 0.75, 40.0, -3.0]), 10.0 ** rng.uniform(-12, -4)
+        b = (target - ref.scores(x[None], kind)[0] + scale * rng.permutation(E)).astype(np.float32)
+        b[rng.random(E) < rng.choice([0, 0.5, 0.9])] = -5 - target
+        s = ref.scores(l, kind) + b.astype(np.float64)
+        sure = np.full(32, np.inf)  # the smallest distance that decides
+        if M < G:
+            by = -np.sort(-s.reshape(32, G, size), 2)
+            group = by[:, :, :2].sum(2) if top2 else by[:, :, 0]
+            order = np.argsort(-group, 1, kind="stable")
+            sure = np.take_along_axis(group, order[:, M - 1:M + 1], 1)
+            sure = sure[:, 0] - sure[:, 1]
+            left = np.ones((32, G), bool)
+            np.put_along_axis(left, order[:, :M], False, 1)
+            s = np.where(left.repeat(size, 1), -np.inf, s)
+        want = np.argsort(-s, 1, kind="stable")
+        v = np.take_along_axis(s, want[:, :k + 1], 1)
+        if v.shape[1] > 1:
+            sure = np.minimum(sure, (v[:, :-1] - v[:, 1:]).min(1))
+        sure = sure > 2.0 ** -46 * max(1, abs(target))
+        say(i, E, k, G, M, kind, top2, pool, target, scale)
+        got = moe.moe_route_scored(torch.from_numpy(l).to(DEV), torch.from_numpy(b).to(DEV), k, G, M, kind, True, top2)[0]
+        bad = np.flatnonzero((got.cpu().numpy() != want[:, :k]).any(1) & sure)
+        assert not len(bad), f"{len(bad)} rows; row {bad[0]}: {got[bad[0]].tolist()} against {want[bad[0], :k]}"
+        rows += int(sure.sum())
+    assert rows > 10000  # 19200, less those too close even for 64 bits
+
+
+def test_sigmoid_weights_keep_their_ratios_far_below_range(moe):
+    """Normalised sigmoid weights of scores that vanish in float32 are the exact ones: exp(l) up to a factor."""
+    d = torch.arange(8) * 0.5
+    l = torch.stack([-200 - d, -1e4 - d, torch.full((8,), -1e10), torch.full((8,), LOWEST[torch.float32])]).float()
+    say("ratios")
+    idx, w = moe.moe_route_scored(l.to(DEV), None, 4, scores="sigmoid")
+    want = np.exp(-0.5 * np.arange(4))
+    want = np.stack([want / want.sum()] * 2 + [np.full(4, 0.25)] * 2)
+    assert idx.tolist() == [[0, 1, 2, 3]] * 4
+    assert (np.abs(w.cpu().double().numpy() - want) <= want * (8 + 8 * 1.5 + 24) * U).all()
