@@ -380,3 +380,25 @@ def test_sigmoid_weights_keep_their_ratios_far_below_range(moe):
     want = np.stack([want / want.sum()] * 2 + [np.full(4, 0.25)] * 2)
     assert idx.tolist() == [[0, 1, 2, 3]] * 4
     assert (np.abs(w.cpu().double().numpy() - want) <= want * (8 + 8 * 1.5 + 24) * U).all()
+
+
+@pytest.mark.parametrize("E", [8, 600])
+def test_nan_logits_and_biases(moe, E):
+    """A NaN logit or bias ranks its expert last under sigmoid, below masked ones; under softmax a NaN or infinite
+    logit leaves ids distinct and in range."""
+    rng = np.random.default_rng(E)
+    l = rng.standard_normal((12, E)).astype(np.float32)
+    l[1, ::2], l[2], l[3, 1:], l[4, 3] = np.nan, np.nan, -np.inf, np.inf
+    l[5, : E - 2], l[5, E - 2:] = np.nan, -np.inf
+    b = (rng.permutation(E) * (0.2 / E / E)).astype(np.float32)
+    for bias in (None, b, np.where(np.arange(E) % 3 == 0, np.nan, b).astype(np.float32)):
+        for G, M, top2 in ((1, 1, False), (4, 3, True), (4, 2, False)):
+            k = 3
+            say(E, bias is not None and np.isnan(bias).any(), G, M, top2)
+            B = None if bias is None else torch.from_numpy(bias).to(DEV)
+            idx = moe.moe_route_scored(torch.from_numpy(l).to(DEV), B, k, G, M, "sigmoid", True, top2)[0].cpu().numpy()
+            if G == 1:  # a group's sum with a NaN in it has no order of its own
+                assert (idx == ref.route(l.astype(np.float64), bias, k, G, M, "sigmoid", True, top2)[0]).all()
+            soft = moe.moe_route_scored(torch.from_numpy(l).to(DEV), B, k, G, M, "softmax", True, top2)[0].cpu().numpy()
+            for ids in (idx, soft):
+                assert all(len(set(r)) == k and min(r) >= 0 and max(r) < E for r in ids.tolist())
