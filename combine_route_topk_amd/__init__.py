@@ -37,6 +37,10 @@ MOE_LOGITS_BF16 = 8
 MOE_PRODUCT_GATED = 1
 MOE_GRAD_FP32 = 1
 MOE_GRAD_ACCUMULATE = 2
+MOE_NORM_FP32 = 1
+MOE_NORM_WEIGHT_FP32 = 2
+MOE_NORM_ACCUMULATE = 4
+MOE_WEIGHTS_FP32 = 1
 MOE_ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 EXPORTS = ("moe_route_topk", "moe_route_topk_grouped", "moe_layout_workspace_size", "moe_dispatch_layout",
@@ -47,7 +51,9 @@ EXPORTS = ("moe_route_topk", "moe_route_topk_grouped", "moe_layout_workspace_siz
            "moe_expert_linear_workspace_size", "moe_expert_linear", "moe_expert_linear_return",
            "moe_expert_return_slots", "moe_hbm_floor", "moe_route_scored", "moe_route_scored_backward",
            "moe_combine_backward", "moe_expert_product", "moe_expert_product_dgrad",
-           "moe_expert_product_wgrad_workspace_size", "moe_expert_product_wgrad", "moe_status_string")
+           "moe_expert_product_wgrad_workspace_size", "moe_expert_product_wgrad", "moe_rms_norm",
+           "moe_rms_norm_backward_workspace_size", "moe_rms_norm_backward", "moe_fp8_quantize_weights",
+           "moe_expert_product_fp8", "moe_expert_product_fp8_dgrad", "moe_status_string")
 
 
 class MoeError(RuntimeError):
@@ -95,6 +101,12 @@ def _load_library() -> ctypes.CDLL:
     lib.moe_expert_product_dgrad.argtypes = [P, P, i32, i64, i32, i32, P, P, i32, u32, P, P]
     lib.moe_expert_product_wgrad_workspace_size.argtypes = [i32, i64, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
     lib.moe_expert_product_wgrad.argtypes = [P, P, P, i32, i64, i32, i32, u32, P, P, P, ctypes.c_size_t, P]
+    lib.moe_rms_norm.argtypes = [P, P, P, i64, i32, f32, u32, P, P, P, P]
+    lib.moe_rms_norm_backward_workspace_size.argtypes = [i64, i32, ctypes.POINTER(ctypes.c_size_t)]
+    lib.moe_rms_norm_backward.argtypes = [P, P, P, i64, i32, f32, u32, P, P, P, P, ctypes.c_size_t, P]
+    lib.moe_fp8_quantize_weights.argtypes = [P, i32, i32, i32, u32, P, P, P, P, P]
+    lib.moe_expert_product_fp8.argtypes = [P, P, i32, i64, i32, i32, P, P, P, P, i32, u32, P, P, P, P]
+    lib.moe_expert_product_fp8_dgrad.argtypes = [P, P, i32, i64, i32, i32, P, P, P, i32, u32, P, P, P]
     lib.moe_status_string.argtypes = [ctypes.c_int]
     lib.moe_status_string.restype = ctypes.c_char_p
     for name in EXPORTS[:-1]:
@@ -534,6 +546,7 @@ def _score_flags(logits: torch.Tensor, scores: str, normalize: bool) -> int:
 
 
 _LOGITS = (torch.float32, torch.bfloat16)
+_STREAM = (torch.float32, torch.bfloat16)  # the residual stream and the norm's and experts' weights
 
 
 def moe_route_scored(logits: torch.Tensor, bias: Optional[torch.Tensor], k: int, n_groups: int = 1,
@@ -703,3 +716,178 @@ def moe_expert_product_wgrad(grad_y: torch.Tensor, x: torch.Tensor, expert_offse
             None if workspace is None else _shaped(workspace, "workspace", workspace.shape, (torch.uint8,), dev),
             0 if workspace is None else workspace.numel(), _stream(None)))
     return grad_W
+
+
+_U8 = (torch.uint8,)
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 fp8: bool = False, need_y: bool = True, total: Optional[torch.Tensor] = None,
+                 y: Optional[torch.Tensor] = None, y8: Optional[torch.Tensor] = None, stream=None):
+    """(total, y, y8): x + residual, its RMS norm in bf16, and the norm as FP8
+    rows [T, moe_fp8_row_bytes(H)] uint8 (see moe_rms_norm). x and residual are
+    bf16 or float32, total is of their type (x itself without residual; it may
+    be given as x or residual). need_y False leaves y out (None); y8 is made
+    when fp8 is set or it is given."""
+    T, H = _need(x, "x", 2).shape
+    dev, dt = x.device, x.dtype
+    fp32 = dt == torch.float32
+    if total is not None and residual is None:
+        raise ValueError("total is written with residual only")
+    with _on(dev, stream):
+        if residual is not None and total is None:
+            total = torch.empty_like(x)
+        if need_y and y is None:
+            y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        if fp8 and y8 is None:
+            y8 = torch.empty((T, moe_fp8_row_bytes(H)), dtype=torch.uint8, device=dev)
+        y = y if need_y else None
+        row = (T, moe_fp8_row_bytes(H)) if y8 is not None else None
+        _check("moe_rms_norm", lib.moe_rms_norm(
+            _ptr(x, _STREAM, "x", 2), _shaped(residual, "residual", (T, H), (dt,), dev),
+            _shaped(weight, "weight", (H,), _STREAM, dev), T, H, eps,
+            (MOE_NORM_FP32 if fp32 else 0) | (MOE_NORM_WEIGHT_FP32 if weight.dtype == torch.float32 else 0),
+            _shaped(total, "total", (T, H), (dt,), dev), _shaped(y, "y", (T, H), _BF16, dev),
+            _shaped(y8, "y8", row, _U8, dev), _stream(None)))
+    return (x if residual is None else total), y, y8
+
+
+def moe_rms_norm_backward_workspace_size(T: int, H: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_rms_norm_backward_workspace_size",
+           lib.moe_rms_norm_backward_workspace_size(T, H, ctypes.byref(n)))
+    return n.value
+
+
+def moe_rms_norm_backward(grad_y: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                          grad_total: Optional[torch.Tensor] = None, grad_x: Optional[torch.Tensor] = None,
+                          grad_weight: Optional[torch.Tensor] = None, need_x: bool = True, need_weight: bool = True,
+                          accumulate: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
+    """(grad_x, grad_weight): the norm's gradients for its input (and residual)
+    and its weight, float32 (see moe_rms_norm_backward). total is what
+    moe_rms_norm returned as such; grad_total, of its type, is added to grad_x
+    and may be given as grad_x too. need_x or need_weight False leaves that one
+    out (None). accumulate adds to grad_weight, which must then be given."""
+    T, H = _need(total, "total", 2).shape
+    dev, dt = total.device, total.dtype
+    if need_weight and accumulate and grad_weight is None:
+        raise ValueError("accumulate needs grad_weight")
+    need = moe_rms_norm_backward_workspace_size(T, H)
+    with _on(dev, stream):
+        if need_x and grad_x is None:
+            grad_x = torch.empty_like(total)
+        if need_weight and grad_weight is None:
+            grad_weight = torch.empty(H, dtype=torch.float32, device=dev)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        grad_x, grad_weight = grad_x if need_x else None, grad_weight if need_weight else None
+        _check("moe_rms_norm_backward", lib.moe_rms_norm_backward(
+            _shaped(grad_y, "grad_y", (T, H), _BF16, dev), _ptr(total, _STREAM, "total", 2),
+            _shaped(weight, "weight", (H,), _STREAM, dev), T, H, eps,
+            (MOE_NORM_FP32 if dt == torch.float32 else 0) | (MOE_NORM_ACCUMULATE if accumulate else 0)
+            | (MOE_NORM_WEIGHT_FP32 if weight.dtype == torch.float32 else 0),
+            _shaped(grad_total, "grad_total", (T, H), (dt,), dev), _shaped(grad_x, "grad_x", (T, H), (dt,), dev),
+            _shaped(grad_weight, "grad_weight", (H,), _F32, dev),
+            None if workspace is None else _shaped(workspace, "workspace", workspace.shape, _U8, dev),
+            0 if workspace is None else workspace.numel(), _stream(None)))
+    return grad_x, grad_weight
+
+
+def moe_fp8_quantize_weights(W: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                             scale: Optional[torch.Tensor] = None, transpose: bool = False,
+                             codes_t: Optional[torch.Tensor] = None, scale_t: Optional[torch.Tensor] = None,
+                             stream=None):
+    """(codes, scale, codes_t, scale_t): W [n, O, H] (bf16 or float32) as E4M3
+    codes of its shape with a float32 scale for each block of 128 x 128, and both
+    transposed when transpose is set or they are given, else None (see
+    moe_fp8_quantize_weights). Codes are float8_e4m3fn, or uint8 when given so."""
+    n, O, H = _need(W, "W", 3).shape
+    dev = W.device
+    a, b = (O + 127) // 128, (H + 127) // 128
+    transpose = transpose or codes_t is not None or scale_t is not None
+    with _on(dev, stream):
+        if codes is None:
+            codes = torch.empty((n, O, H), dtype=torch.float8_e4m3fn, device=dev)
+        if scale is None:
+            scale = torch.empty((n, a, b), dtype=torch.float32, device=dev)
+        if transpose and codes_t is None:
+            codes_t = torch.empty((n, H, O), dtype=torch.float8_e4m3fn, device=dev)
+        if transpose and scale_t is None:
+            scale_t = torch.empty((n, b, a), dtype=torch.float32, device=dev)
+        _check("moe_fp8_quantize_weights", lib.moe_fp8_quantize_weights(
+            _ptr(W, _STREAM, "W", 3), n, O, H, MOE_WEIGHTS_FP32 if W.dtype == torch.float32 else 0,
+            _shaped(codes, "codes", (n, O, H), _E4M3, dev), _shaped(scale, "scale", (n, a, b), _F32, dev),
+            _shaped(codes_t, "codes_t", (n, H, O), _E4M3, dev), _shaped(scale_t, "scale_t", (n, b, a), _F32, dev),
+            _stream(None)))
+    return codes, scale, codes_t, scale_t
+
+
+def moe_expert_product_fp8(x: torch.Tensor, expert_offsets: torch.Tensor, W: torch.Tensor, W_scale: torch.Tensor,
+                           bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                           act: str = "none", gated: bool = False, fp8: bool = False, need_y: bool = True,
+                           y: Optional[torch.Tensor] = None, y8: Optional[torch.Tensor] = None,
+                           pre: Optional[torch.Tensor] = None, stream=None):
+    """(y, y8): moe_expert_product on FP8 rows x [max_rows, moe_fp8_row_bytes(H)]
+    uint8 and 8-bit weights W [E_l, O, H] ([E_l, 2 O, H] gated; float8_e4m3fn or
+    uint8) with W_scale, as moe_fp8_quantize_weights makes them (see
+    moe_expert_product_fp8). y is bf16, y8 the same results as FP8 rows, made
+    when fp8 is set or it is given; need_y False leaves y out (None). Rows past
+    the last expert's are not written."""
+    max_rows, row = _need(x, "x", 2).shape
+    dev = x.device
+    El, wide, H = _need(W, "W", 3).shape
+    if gated and wide % 2:
+        raise ValueError("a gated W holds gate and up outputs in equal number")
+    O = wide // 2 if gated else wide
+    if row != moe_fp8_row_bytes(H):
+        raise ValueError(f"x must be [n, {moe_fp8_row_bytes(H)}] bytes, got {list(x.shape)}")
+    with _on(dev, stream):
+        if need_y and y is None:
+            y = torch.empty((max_rows, O), dtype=torch.bfloat16, device=dev)
+        if fp8 and y8 is None:
+            y8 = torch.empty((max_rows, moe_fp8_row_bytes(O)), dtype=torch.uint8, device=dev)
+        y = y if need_y else None
+        row8 = (max_rows, moe_fp8_row_bytes(O)) if y8 is not None else None
+        _check("moe_expert_product_fp8", lib.moe_expert_product_fp8(
+            _ptr(x, _U8, "x", 2), _shaped(expert_offsets, "expert_offsets", (El + 1,), _I32, dev), El, max_rows, H, O,
+            _shaped(W, "W", (El, wide, H), _E4M3, dev),
+            _shaped(W_scale, "W_scale", (El, (wide + 127) // 128, (H + 127) // 128), _F32, dev),
+            _shaped(bias, "bias", (El, wide), _BF16, dev), _shaped(residual, "residual", (max_rows, O), _BF16, dev),
+            _act(act), MOE_PRODUCT_GATED if gated else 0, _shaped(pre, "pre", (max_rows, wide), _BF16, dev),
+            _shaped(y, "y", (max_rows, O), _BF16, dev), _shaped(y8, "y8", row8, _U8, dev), _stream(None)))
+    return y, y8
+
+
+def moe_expert_product_fp8_dgrad(grad_y: torch.Tensor, expert_offsets: torch.Tensor, W_t: torch.Tensor,
+                                 W_t_scale: torch.Tensor, pre: Optional[torch.Tensor] = None, act: str = "none",
+                                 gated: bool = False, fp8: bool = False, need_x: bool = True,
+                                 grad_x: Optional[torch.Tensor] = None, grad_x8: Optional[torch.Tensor] = None,
+                                 stream=None):
+    """(grad_x, grad_x8): FP8 rows grad_y [max_rows, moe_fp8_row_bytes(O)] times W,
+    given transposed (W_t [E_l, H, O] and W_t_scale, moe_fp8_quantize_weights'
+    codes_t and scale_t), through the activation (of pre) that made the product's
+    input (see moe_expert_product_fp8_dgrad). grad_x is [max_rows, H] bf16 ([.., 2 H]
+    gated), grad_x8 the same as FP8 rows, made when fp8 is set or it is given;
+    need_x False leaves grad_x out (None)."""
+    max_rows, row = _need(grad_y, "grad_y", 2).shape
+    dev = grad_y.device
+    El, H, O = _need(W_t, "W_t", 3).shape
+    wide = 2 * H if gated else H
+    if row != moe_fp8_row_bytes(O):
+        raise ValueError(f"grad_y must be [n, {moe_fp8_row_bytes(O)}] bytes, got {list(grad_y.shape)}")
+    with _on(dev, stream):
+        if need_x and grad_x is None:
+            grad_x = torch.empty((max_rows, wide), dtype=torch.bfloat16, device=dev)
+        if fp8 and grad_x8 is None:
+            grad_x8 = torch.empty((max_rows, moe_fp8_row_bytes(wide)), dtype=torch.uint8, device=dev)
+        grad_x = grad_x if need_x else None
+        row8 = (max_rows, moe_fp8_row_bytes(wide)) if grad_x8 is not None else None
+        _check("moe_expert_product_fp8_dgrad", lib.moe_expert_product_fp8_dgrad(
+            _ptr(grad_y, _U8, "grad_y", 2), _shaped(expert_offsets, "expert_offsets", (El + 1,), _I32, dev), El,
+            max_rows, O, H, _shaped(W_t, "W_t", (El, H, O), _E4M3, dev),
+            _shaped(W_t_scale, "W_t_scale", (El, (H + 127) // 128, (O + 127) // 128), _F32, dev),
+            _shaped(pre, "pre", (max_rows, wide), _BF16, dev), _act(act), MOE_PRODUCT_GATED if gated else 0,
+            _shaped(grad_x, "grad_x", (max_rows, wide), _BF16, dev),
+            _shaped(grad_x8, "grad_x8", row8, _U8, dev), _stream(None)))
+    return grad_x, grad_x8

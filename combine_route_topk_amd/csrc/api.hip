@@ -135,6 +135,24 @@ moe_status_t check_product(int32_t El, int64_t max_rows, int32_t H, int32_t O)
     return s != MOE_OK ? s : check_hidden(O);
 }
 
+// Sizes of the products on FP8 rows: whole blocks of 32 values in and out.
+moe_status_t check_product_fp8(int32_t E_l, int64_t max_rows, int32_t H, int32_t O)
+{
+    const moe_status_t s = check_product(E_l, max_rows, H, O);
+    if (s != MOE_OK)
+        return s;
+    return H % 32 || O % 32 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+moe_status_t check_norm(int64_t T, int32_t H, float eps, uint32_t flags, uint32_t allowed)
+{
+    if (T < 0 || (flags & ~allowed) || !(eps >= 0.f) || !(eps - eps == 0.f))
+        return MOE_ERR_INVALID_ARG;
+    if (T >= kMaxAssignments)
+        return MOE_ERR_UNSUPPORTED;
+    return check_hidden(H);
+}
+
 bool known_act(int32_t act) { return act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH; }
 
 }  // namespace
@@ -708,6 +726,143 @@ moe_status_t moe_expert_product_wgrad(const uint16_t *grad_y, const uint16_t *x,
         grad_y, x, expert_offsets, E_l, max_rows, O, H, (flags & MOE_GRAD_FP32) != 0,
         (flags & MOE_GRAD_ACCUMULATE) != 0, grad_W, grad_bias, workspace,
         static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_rms_norm(const void *x, const void *residual, const void *weight, int64_t T,
+                          int32_t H, float eps, uint32_t flags, void *total, uint16_t *y,
+                          uint8_t *y8, void *stream)
+{
+    moe_status_t s = check_norm(T, H, eps, flags, MOE_NORM_FP32 | MOE_NORM_WEIGHT_FP32);
+    if (s != MOE_OK)
+        return s;
+    if (y8 && H % 32)
+        return MOE_ERR_UNSUPPORTED;
+    if (T == 0)
+        return MOE_OK;
+    if (!x || !weight || (!y && !y8) || (residual != nullptr) != (total != nullptr))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(total, 16) ||
+        !aligned(y, 16) || !aligned(y8, 16))
+        return MOE_ERR_INVALID_ARG;
+    const moe::NormArgs p = {x, residual, weight, (flags & MOE_NORM_WEIGHT_FP32) != 0, T, H, eps,
+                             total, y, y8, moe::fp8_row_bytes(H)};
+    return from_hip(moe::launch_rms_norm(p, (flags & MOE_NORM_FP32) != 0,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_rms_norm_backward_workspace_size(int64_t T, int32_t H, size_t *bytes)
+{
+    if (!bytes)
+        return MOE_ERR_INVALID_ARG;
+    const moe_status_t s = check_norm(T, H, 0.f, 0, 0);
+    if (s != MOE_OK)
+        return s;
+    *bytes = moe::rms_norm_backward_workspace_bytes(T, H);
+    return MOE_OK;
+}
+
+moe_status_t moe_rms_norm_backward(const uint16_t *grad_y, const void *total, const void *weight,
+                                   int64_t T, int32_t H, float eps, uint32_t flags,
+                                   const void *grad_total, void *grad_x, float *grad_weight,
+                                   void *workspace, size_t workspace_bytes, void *stream)
+{
+    moe_status_t s = check_norm(T, H, eps, flags,
+                                MOE_NORM_FP32 | MOE_NORM_WEIGHT_FP32 | MOE_NORM_ACCUMULATE);
+    if (s != MOE_OK)
+        return s;
+    if (T == 0 && !grad_weight)
+        return MOE_OK;
+    if ((T > 0 && (!grad_y || !total || !weight)) || (!grad_x && !grad_weight))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(grad_y, 16) || !aligned(total, 16) || !aligned(weight, 16) ||
+        !aligned(grad_total, 16) || !aligned(grad_x, 16) || !aligned(grad_weight, 4))
+        return MOE_ERR_INVALID_ARG;
+    const size_t need = moe::rms_norm_backward_workspace_bytes(T, H);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+        return MOE_ERR_WORKSPACE;
+    const moe::NormGradArgs p = {grad_y, total, weight, grad_total,
+                                 (flags & MOE_NORM_WEIGHT_FP32) != 0, T, H, eps, grad_x,
+                                 nullptr, nullptr};
+    return from_hip(moe::launch_rms_norm_backward(p, (flags & MOE_NORM_FP32) != 0,
+                                                  (flags & MOE_NORM_ACCUMULATE) != 0, grad_weight,
+                                                  workspace, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_fp8_quantize_weights(const void *W, int32_t n, int32_t O, int32_t H,
+                                      uint32_t flags, uint8_t *codes, float *scale,
+                                      uint8_t *codes_t, float *scale_t, void *stream)
+{
+    if (n < 0 || (flags & ~MOE_WEIGHTS_FP32) || (codes_t != nullptr) != (scale_t != nullptr))
+        return MOE_ERR_INVALID_ARG;
+    if (n > moe::kMaxLocalExperts || O < 32 || O % 32 || O > 2 * kMaxH || H < 32 || H % 32 ||
+        H > kMaxH)
+        return MOE_ERR_UNSUPPORTED;
+    if (n == 0)
+        return MOE_OK;
+    if (!W || !codes || !scale)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(W, 16) || !aligned(codes, 16) || !aligned(codes_t, 16) || !aligned(scale, 4) ||
+        !aligned(scale_t, 4))
+        return MOE_ERR_INVALID_ARG;
+    const moe::QuantizeArgs p = {W, O, H, codes, scale, codes_t, scale_t, 0};
+    return from_hip(moe::launch_quantize_weights(p, n, (flags & MOE_WEIGHTS_FP32) != 0,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_expert_product_fp8(const uint8_t *x, const int32_t *expert_offsets, int32_t E_l,
+                                    int64_t max_rows, int32_t H, int32_t O, const uint8_t *W,
+                                    const float *W_scale, const uint16_t *bias,
+                                    const uint16_t *residual, int32_t act, uint32_t flags,
+                                    uint16_t *pre, uint16_t *y, uint8_t *y8, void *stream)
+{
+    moe_status_t s = check_product_fp8(E_l, max_rows, H, O);
+    if (s != MOE_OK)
+        return s;
+    if ((flags & ~MOE_PRODUCT_GATED) || !known_act(act))
+        return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0)
+        return MOE_OK;
+    if (!x || !expert_offsets || !W || !W_scale || (!y && !y8))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(W, 16) || !aligned(W_scale, 4) || !aligned(y, 16) ||
+        !aligned(y8, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(pre, 16) ||
+        !aligned(expert_offsets, 4))
+        return MOE_ERR_INVALID_ARG;
+    const moe::Product8Args p = {x, expert_offsets, W, W_scale, bias, residual, nullptr, pre, y,
+                                 y8, E_l, (int32_t)max_rows, H, O, moe::fp8_row_bytes(H),
+                                 moe::fp8_row_bytes(O)};
+    return from_hip(moe::launch_product_fp8(p, act, (flags & MOE_PRODUCT_GATED) != 0, false,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_expert_product_fp8_dgrad(const uint8_t *grad_y, const int32_t *expert_offsets,
+                                          int32_t E_l, int64_t max_rows, int32_t O, int32_t H,
+                                          const uint8_t *W_t, const float *W_t_scale,
+                                          const uint16_t *pre, int32_t act, uint32_t flags,
+                                          uint16_t *grad_x, uint8_t *grad_x8, void *stream)
+{
+    moe_status_t s = check_product_fp8(E_l, max_rows, H, O);
+    if (s != MOE_OK)
+        return s;
+    if ((flags & ~MOE_PRODUCT_GATED) || !known_act(act))
+        return MOE_ERR_INVALID_ARG;
+    const bool gated = (flags & MOE_PRODUCT_GATED) != 0;
+    if (gated && grad_x8 && 2 * H > kMaxH)
+        return MOE_ERR_UNSUPPORTED;
+    if (!pre && (flags || act != MOE_ACT_NONE) && max_rows > 0)
+        return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0)
+        return MOE_OK;
+    if (!grad_y || !expert_offsets || !W_t || !W_t_scale || (!grad_x && !grad_x8))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(grad_y, 16) || !aligned(W_t, 16) || !aligned(W_t_scale, 4) || !aligned(pre, 16) ||
+        !aligned(grad_x, 16) || !aligned(grad_x8, 16) || !aligned(expert_offsets, 4))
+        return MOE_ERR_INVALID_ARG;
+    const moe::Product8Args p = {grad_y, expert_offsets, W_t, W_t_scale, nullptr, nullptr, pre,
+                                 nullptr, grad_x, grad_x8, E_l, (int32_t)max_rows, O, H,
+                                 moe::fp8_row_bytes(O), moe::fp8_row_bytes(gated ? 2 * H : H)};
+    return from_hip(moe::launch_product_fp8(p, act, gated, true,
+                                            static_cast<hipStream_t>(stream)));
 }
 
 moe_status_t moe_hbm_floor(const void *src, int64_t read_bytes, void *dst, int64_t write_bytes,

@@ -145,6 +145,61 @@ hipError_t launch_expert_wgrad(const uint16_t *grad_y, const uint16_t *x, const 
                                bool accumulate, void *grad_W, float *grad_bias, void *workspace,
                                hipStream_t stream);
 
+// The RMS norm and its gradient (norm.hip). x, residual, total and their
+// gradients are float32 or bf16; the weight is float32 or bf16.
+struct NormArgs {
+    const void *x, *residual, *weight;
+    bool weight_fp32;
+    int64_t T;
+    int32_t H;
+    float eps;
+    void *total;       // written where residual is given
+    uint16_t *y;       // or NULL
+    uint8_t *y8;       // or NULL
+    int64_t y8_bytes;  // bytes of an FP8 row
+};
+hipError_t launch_rms_norm(const NormArgs &p, bool fp32, hipStream_t stream);
+struct NormGradArgs {
+    const void *grad_y, *t, *weight, *grad_total;
+    bool weight_fp32;
+    int64_t T;
+    int32_t H;
+    float eps;
+    void *grad_x;            // or NULL
+    float *partial, *stats;  // in the workspace
+};
+size_t rms_norm_backward_workspace_bytes(int64_t T, int32_t H);
+hipError_t launch_rms_norm_backward(NormGradArgs p, bool fp32, bool accumulate, float *grad_weight,
+                                    void *workspace, hipStream_t stream);
+
+// Weights in 8 bits with a scale for each block of 128 x 128 (quantize_weights.hip).
+struct QuantizeArgs {
+    const void *W;
+    int32_t O, H;
+    uint8_t *codes;
+    float *scale;
+    uint8_t *codes_t;  // or NULL, scale_t with it
+    float *scale_t;
+    int64_t first;     // matrix of the launch's first block
+};
+hipError_t launch_quantize_weights(QuantizeArgs p, int64_t n, bool fp32, hipStream_t stream);
+
+// The experts' products on FP8 rows and their input gradient (product_fp8.hip).
+// N: output columns before a gate doubles them.
+struct Product8Args {
+    const uint8_t *a;   // FP8 rows of K values
+    const int32_t *off;
+    const uint8_t *W;
+    const float *scale;
+    const uint16_t *bias, *residual, *pre_in;
+    uint16_t *pre_out, *out;  // out or out8 may be NULL
+    uint8_t *out8;
+    int32_t El, max_rows, K, N;
+    int64_t a_bytes, out8_bytes;  // bytes of a row
+};
+hipError_t launch_product_fp8(const Product8Args &p, int32_t act, bool gated, bool grad, hipStream_t stream);
+hipError_t launch_product_fp8_few(const Product8Args &p, int32_t act, bool gated, hipStream_t stream);
+
 // Synthetic floor: a contiguous streaming read and write (floor.hip).
 hipError_t launch_hbm_floor(const void *src, int64_t read_bytes, void *dst, int64_t write_bytes,
                             bool nt_store, hipStream_t stream);

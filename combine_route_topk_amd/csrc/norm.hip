@@ -1,0 +1,513 @@
+// norm.hip -- the RMS norm in front of a layer, with the residual's addition,
+// and its gradient.
+//
+//   t = round(x + residual);  y = t * rsqrt(mean(t^2) + eps) * weight
+//   dt = r (g - t r^2 mean(g t)) + grad_total,  g = grad_y * weight
+//   grad_weight = sum over tokens of grad_y t r,  r = rsqrt(mean(t^2) + eps)
+//
+// Bound by HBM: a row is read once, held in registers across its sum, and
+// written once in every form that is asked for (bf16, FP8 rows, the sum).
+// The norm is of t as it is stored, so that the gradient, which reads t,
+// differentiates the very function that ran; r is recomputed there from the
+// row that is in registers anyway.
+#include "fp8_device.hpp"
+#include "launch.hpp"
+
+namespace moe {
+namespace {
+
+// lane 63 ends with the wave's sum; the order is fixed
+__device__ __forceinline__ float wave_sum(float v)
+{
+    auto add = [](float a, uint32_t b) { return a + __uint_as_float(b); };
+    v = add(v, dpp::mov<dpp::kQuadSwap1>(__float_as_uint(v), 0u));
+    v = add(v, dpp::mov<dpp::kQuadSwap2>(__float_as_uint(v), 0u));
+    v = add(v, dpp::mov<dpp::kRowHalfMirror>(__float_as_uint(v), 0u));
+    v = add(v, dpp::mov<dpp::kRowMirror>(__float_as_uint(v), 0u));
+    v = add(v, dpp::mov<dpp::kRowBcast15, 0xA>(__float_as_uint(v), 0u));
+    v = add(v, dpp::mov<dpp::kRowBcast31, 0xC>(__float_as_uint(v), 0u));
+    return __uint_as_float(readlane_u32(__float_as_uint(v), kWave - 1));
+}
+
+// Eight consecutive values as they lie in memory, bf16 or float32.
+template <bool FP32>
+struct Raw8 {
+    u32x4 q[FP32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void *p, int64_t chunk)
+    {
+        const u32x4 *s = static_cast<const u32x4 *>(p) + chunk * (FP32 ? 2 : 1);
+        q[0] = s[0];
+        if (FP32)
+            q[FP32 ? 1 : 0] = s[1];
+    }
+    __device__ __forceinline__ void store(void *p, int64_t chunk) const
+    {
+        u32x4 *s = static_cast<u32x4 *>(p) + chunk * (FP32 ? 2 : 1);
+        s[0] = q[0];
+        if (FP32)
+            s[1] = q[FP32 ? 1 : 0];
+    }
+    __device__ __forceinline__ float get(int i) const
+    {
+        if (FP32)
+            return __uint_as_float(q[FP32 ? i >> 2 : 0][i & 3]);
+        return i & 1 ? bf16_hi(q[0][i >> 1]) : bf16_lo(q[0][i >> 1]);
+    }
+    __device__ __forceinline__ void set(const float (&v)[8])
+    {
+#pragma unroll
+        for (int i = 0; i < (FP32 ? 8 : 4); ++i)
+            q[FP32 ? i >> 2 : 0][i & 3] = FP32 ? __float_as_uint(v[i]) : pack_bf16x2(v[2 * i & 7], v[(2 * i + 1) & 7]);
+    }
+};
+
+// The weight's type is a branch, the same for every lane.
+__device__ __forceinline__ void load_weight(const void *w, bool fp32, int64_t chunk, float (&v)[8])
+{
+    if (fp32) {
+        Raw8<true> r;
+        r.load(w, chunk);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = r.get(i);
+    } else {
+        Raw8<false> r;
+        r.load(w, chunk);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = r.get(i);
+    }
+}
+
+// WPR waves take a row, each lane CH chunks of eight columns; a block of at
+// least four waves.
+constexpr int norm_threads(int wpr) { return wpr < 4 ? 256 : wpr * kWave; }
+constexpr int kScaleLine = 128;  // scale bytes of 4096 values
+
+template <bool FP32, int WPR, int CH>
+__global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_kernel(NormArgs p)
+{
+    constexpr int kRows = norm_threads(WPR) / kWave / WPR;
+    constexpr int kLines = (WPR * CH * 512 + 4095) / 4096;
+    __shared__ float part[2][kRows][WPR];
+    __shared__ __attribute__((aligned(16))) uint8_t scales[kRows][kLines * kScaleLine];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int slot = wave / WPR, wr = wave % WPR;  // the wave's row of the block, and its place in it
+    const int32_t C = p.H / 8;
+    const int32_t pad = (p.H + 4095) / 4096 * kScaleLine;  // scale bytes of a row
+    if (p.y8) {  // padding stays zero: no wave writes it below
+        for (int i = threadIdx.x; i < kRows * kLines * kScaleLine / 4; i += norm_threads(WPR))
+            reinterpret_cast<uint32_t *>(scales)[i] = 0;
+        __syncthreads();
+    }
+    int parity = 0;
+    for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += (int64_t)gridDim.x * kRows) {
+        const int64_t t = t0 + slot;
+        const bool valid = t < p.T;
+        Raw8<FP32> h[CH];
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int32_t c = (i * WPR + wr) * kWave + lane;
+            if (valid && c < C)
+                h[i].load(p.x, t * C + c);
+        }
+        if (p.residual) {
+            Raw8<FP32> r[CH];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int32_t c = (i * WPR + wr) * kWave + lane;
+                if (valid && c < C)
+                    r[i].load(p.residual, t * C + c);
+            }
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int32_t c = (i * WPR + wr) * kWave + lane;
+                if (valid && c < C) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = h[i].get(e) + r[i].get(e);
+                    h[i].set(v);
+                    h[i].store(p.total, t * C + c);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int32_t c = (i * WPR + wr) * kWave + lane;
+            if (valid && c < C)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sum = fmaf(h[i].get(e), h[i].get(e), sum);
+        }
+        sum = wave_sum(sum);
+        if (WPR > 1) {
+            if (lane == 0)
+                part[parity][slot][wr] = sum;
+            __syncthreads();
+            sum = part[parity][slot][0];
+#pragma unroll
+            for (int u = 1; u < WPR; ++u)
+                sum += part[parity][slot][u];
+            parity ^= 1;
+        }
+        const float r = rsqrtf(sum / (float)p.H + p.eps);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int32_t c = (i * WPR + wr) * kWave + lane;
+            if (!valid || c >= C)
+                continue;
+            float v[8];
+            load_weight(p.weight, p.weight_fp32, c, v);
+            float m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[e] *= h[i].get(e) * r;
+                m = max_abs(m, v[e]);
+            }
+            if (p.y) {
+                Raw8<false> o;
+                o.set(v);
+                o.store(p.y, t * C + c);
+            }
+            if (p.y8) {
+                // H is a multiple of 32: the four lanes of a block are all here
+                m = fmaxf(m, __uint_as_float(dpp::mov<dpp::kQuadSwap1>(__float_as_uint(m), 0u)));
+                m = fmaxf(m, __uint_as_float(dpp::mov<dpp::kQuadSwap2>(__float_as_uint(m), 0u)));
+                const int32_t e = fp8_exponent(m);
+                const float mul = fp8_multiplier(e);
+                const u32x2 codes = {fp8_encode4(v[0], v[1], v[2], v[3], mul), fp8_encode4(v[4], v[5], v[6], v[7], mul)};
+                reinterpret_cast<u32x2 *>(p.y8 + t * p.y8_bytes)[c] = codes;
+                if ((lane & 3) == 0)
+                    scales[slot][c >> 2] = (uint8_t)(e + 127);
+            }
+        }
+        if (p.y8) {
+            if (WPR > 1)
+                __syncthreads();
+            else
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            const int i = wr * kWave + lane;  // the row's scale bytes in whole lines
+            if (valid && i < pad / 16)
+                reinterpret_cast<u32x4 *>(p.y8 + t * p.y8_bytes + p.H)[i] = reinterpret_cast<const u32x4 *>(scales[slot])[i];
+            if (WPR > 1)
+                __syncthreads();
+            else
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+    }
+}
+
+// r and mean(g t) r^2 of one row in every lane of its waves
+struct RowStats {
+    float r, c;
+};
+
+// The gradient of rows blockIdx.x * kRows + slot, and further ones, in columns
+// from blockIdx.y * (the columns that the waves cover). GIVEN: the row's
+// statistics are read from p.stats, since a block covers only a part of the row.
+template <bool FP32, int WPR, int CH, bool GIVEN>
+__global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_backward_kernel(NormGradArgs p)
+{
+    constexpr int kRows = norm_threads(WPR) / kWave / WPR;
+    __shared__ float part[2][2][kRows][WPR];
+    __shared__ float sums[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? WPR * CH * 512 : 1];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int slot = wave / WPR, wr = wave % WPR;
+    const int32_t C = p.H / 8, c0 = GIVEN ? blockIdx.y * (WPR * CH * kWave) : 0;
+    float acc[CH][8];
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            acc[i][e] = 0.f;
+    int parity = 0;
+    for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += (int64_t)gridDim.x * kRows) {
+        const int64_t t = t0 + slot;
+        const bool valid = t < p.T;
+        Raw8<FP32> h[CH];
+        Raw8<false> g[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int32_t c = c0 + (i * WPR + wr) * kWave + lane;
+            if (valid && c < C) {
+                h[i].load(p.t, t * C + c);
+                g[i].load(p.grad_y, t * C + c);
+            }
+        }
+        RowStats s = {0.f, 0.f};
+        if (GIVEN) {
+            if (valid)
+                s = RowStats{p.stats[2 * t], p.stats[2 * t + 1]};
+        } else {
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int32_t c = c0 + (i * WPR + wr) * kWave + lane;
+                if (valid && c < C) {
+                    float w[8];
+                    load_weight(p.weight, p.weight_fp32, c, w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        s0 = fmaf(h[i].get(e), h[i].get(e), s0);
+                        s1 = fmaf(g[i].get(e) * w[e], h[i].get(e), s1);
+                    }
+                }
+            }
+            s0 = wave_sum(s0);
+            s1 = wave_sum(s1);
+            if (WPR > 1) {
+                if (lane == 0) {
+                    part[parity][0][slot][wr] = s0;
+                    part[parity][1][slot][wr] = s1;
+                }
+                __syncthreads();
+                s0 = part[parity][0][slot][0];
+                s1 = part[parity][1][slot][0];
+#pragma unroll
+                for (int u = 1; u < WPR; ++u) {
+                    s0 += part[parity][0][slot][u];
+                    s1 += part[parity][1][slot][u];
+                }
+                parity ^= 1;
+            }
+            s.r = rsqrtf(s0 / (float)p.H + p.eps);
+            s.c = s1 / (float)p.H * s.r * s.r;
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int32_t c = c0 + (i * WPR + wr) * kWave + lane;
+            if (!valid || c >= C)
+                continue;
+            if (p.grad_x) {
+                float w[8], v[8];
+                load_weight(p.weight, p.weight_fp32, c, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = s.r * (g[i].get(e) * w[e] - h[i].get(e) * s.c);
+                if (p.grad_total) {
+                    Raw8<FP32> d;
+                    d.load(p.grad_total, t * C + c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] += d.get(e);
+                }
+                Raw8<FP32> o;
+                o.set(v);
+                o.store(p.grad_x, t * C + c);
+            }
+            if (p.partial)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    acc[i][e] = fmaf(g[i].get(e), h[i].get(e) * s.r, acc[i][e]);
+        }
+    }
+    if (!p.partial)
+        return;
+    // the block's rows together, in the order of its waves
+    if (kRows > 1) {
+        if (slot > 0)
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sums[slot - 1][((i * WPR + wr) * 8 + e) * kWave + lane] = acc[i][e];
+        __syncthreads();
+        if (slot > 0)
+            return;
+#pragma unroll
+        for (int u = 0; u < kRows - 1; ++u)
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    acc[i][e] += sums[u][((i * WPR + wr) * 8 + e) * kWave + lane];
+    }
+    float *out = p.partial + (int64_t)blockIdx.x * p.H;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int32_t c = c0 + (i * WPR + wr) * kWave + lane;
+        if (c < C) {
+            reinterpret_cast<u32x4 *>(out)[2 * c] = u32x4{__float_as_uint(acc[i][0]), __float_as_uint(acc[i][1]),
+                                                          __float_as_uint(acc[i][2]), __float_as_uint(acc[i][3])};
+            reinterpret_cast<u32x4 *>(out)[2 * c + 1] = u32x4{__float_as_uint(acc[i][4]), __float_as_uint(acc[i][5]),
+                                                              __float_as_uint(acc[i][6]), __float_as_uint(acc[i][7])};
+        }
+    }
+}
+
+// Statistics of rows too wide for one block's registers: a block per row.
+constexpr int kStatThreads = 512;
+template <bool FP32>
+__global__ __launch_bounds__(kStatThreads) void rms_norm_stats_kernel(NormGradArgs p)
+{
+    __shared__ float part[2][kStatThreads / kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int32_t C = p.H / 8;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        float s0 = 0.f, s1 = 0.f;
+        for (int32_t c = threadIdx.x; c < C; c += kStatThreads) {
+            Raw8<FP32> h;
+            Raw8<false> g;
+            float w[8];
+            h.load(p.t, t * C + c);
+            g.load(p.grad_y, t * C + c);
+            load_weight(p.weight, p.weight_fp32, c, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s0 = fmaf(h.get(e), h.get(e), s0);
+                s1 = fmaf(g.get(e) * w[e], h.get(e), s1);
+            }
+        }
+        s0 = wave_sum(s0);
+        s1 = wave_sum(s1);
+        __syncthreads();  // the row before has been read
+        if (lane == 0) {
+            part[0][wave] = s0;
+            part[1][wave] = s1;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            s0 = s1 = 0.f;
+            for (int u = 0; u < kStatThreads / kWave; ++u) {
+                s0 += part[0][u];
+                s1 += part[1][u];
+            }
+            const float r = rsqrtf(s0 / (float)p.H + p.eps);
+            p.stats[2 * t] = r;
+            p.stats[2 * t + 1] = s1 / (float)p.H * r * r;
+        }
+    }
+}
+
+// grad_weight[h] (+)= sum of the blocks' partial sums, in the blocks' order
+// within each wave and then the waves': 64 columns a block.
+constexpr int kJoinWaves = 16;
+__global__ __launch_bounds__(kJoinWaves *kWave) void rms_norm_join_kernel(const float *__restrict__ partial,
+                                                                          int32_t blocks, int32_t H, bool accumulate,
+                                                                          float *__restrict__ grad_weight)
+{
+    __shared__ float part[kJoinWaves][kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int32_t h = blockIdx.x * kWave + lane;
+    const int32_t each = (blocks + kJoinWaves - 1) / kJoinWaves;
+    const int32_t end = min(blocks, (wave + 1) * each);
+    float s = 0.f;
+    if (h < H)
+#pragma unroll 8
+        for (int32_t b = wave * each; b < end; ++b)
+            s += partial[(int64_t)b * H + h];
+    part[wave][lane] = s;
+    __syncthreads();
+    if (wave || h >= H)
+        return;
+#pragma unroll
+    for (int u = 1; u < kJoinWaves; ++u)
+        s += part[u][lane];
+    grad_weight[h] = accumulate ? grad_weight[h] + s : s;
+}
+
+constexpr int32_t kNormWide = 16384;  // wider rows' gradients take their statistics first
+constexpr int32_t kNormGradBlocks = 1024;
+
+int32_t grad_rows_per_block(int32_t H) { return H <= 2048 ? 4 : 1; }
+int32_t grad_blocks(int64_t T, int32_t H)
+{
+    const int32_t rows = grad_rows_per_block(H);
+    const int64_t n = (T + rows - 1) / rows;
+    return (int32_t)(n < kNormGradBlocks ? n : kNormGradBlocks);
+}
+
+template <bool FP32, int WPR, int CH>
+hipError_t launch_norm(const NormArgs &p, hipStream_t stream)
+{
+    constexpr int kRows = norm_threads(WPR) / kWave / WPR;
+    const int64_t blocks = (p.T + kRows - 1) / kRows;
+    hipLaunchKernelGGL((rms_norm_kernel<FP32, WPR, CH>), dim3((unsigned)(blocks < kMaxRowBlocks ? blocks : kMaxRowBlocks)),
+                       dim3(norm_threads(WPR)), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <bool FP32>
+hipError_t norm_by_width(const NormArgs &p, hipStream_t stream)
+{
+    if (p.H <= 512)
+        return launch_norm<FP32, 1, 1>(p, stream);
+    if (p.H <= 1024)
+        return launch_norm<FP32, 1, 2>(p, stream);
+    if (p.H <= 2048)
+        return launch_norm<FP32, 1, 4>(p, stream);
+    if (p.H <= 4096)
+        return launch_norm<FP32, 4, 2>(p, stream);
+    if (p.H <= 8192)
+        return launch_norm<FP32, 4, 4>(p, stream);
+    if (p.H <= 16384)
+        return launch_norm<FP32, 8, 4>(p, stream);
+    if (p.H <= 32768)
+        return launch_norm<FP32, 16, 4>(p, stream);
+    return launch_norm<FP32, 16, 8>(p, stream);
+}
+
+template <bool FP32, int WPR, int CH, bool GIVEN = false>
+hipError_t launch_norm_grad(const NormGradArgs &p, int32_t blocks, hipStream_t stream)
+{
+    const dim3 grid((unsigned)blocks, GIVEN ? (unsigned)((p.H + WPR * CH * 512 - 1) / (WPR * CH * 512)) : 1);
+    hipLaunchKernelGGL((rms_norm_backward_kernel<FP32, WPR, CH, GIVEN>), grid, dim3(norm_threads(WPR)), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <bool FP32>
+hipError_t norm_grad_by_width(const NormGradArgs &p, hipStream_t stream)
+{
+    const int32_t blocks = grad_blocks(p.T, p.H);
+    if (p.H <= 512)
+        return launch_norm_grad<FP32, 1, 1>(p, blocks, stream);
+    if (p.H <= 1024)
+        return launch_norm_grad<FP32, 1, 2>(p, blocks, stream);
+    if (p.H <= 2048)
+        return launch_norm_grad<FP32, 1, 4>(p, blocks, stream);
+    if (p.H <= 4096)
+        return launch_norm_grad<FP32, 4, 2>(p, blocks, stream);
+    if (p.H <= 8192)
+        return launch_norm_grad<FP32, 4, 4>(p, blocks, stream);
+    if (p.H <= kNormWide)
+        return launch_norm_grad<FP32, 8, 4>(p, blocks, stream);
+    hipLaunchKernelGGL(rms_norm_stats_kernel<FP32>, dim3((unsigned)(p.T < kMaxRowBlocks ? p.T : kMaxRowBlocks)),
+                       dim3(kStatThreads), 0, stream, p);
+    const hipError_t err = hipGetLastError();
+    return err == hipSuccess ? launch_norm_grad<FP32, 4, 4, true>(p, blocks, stream) : err;
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs &p, bool fp32, hipStream_t stream)
+{
+    return fp32 ? norm_by_width<true>(p, stream) : norm_by_width<false>(p, stream);
+}
+
+// partial sums of the weight's gradient, then the statistics of wide rows
+size_t rms_norm_backward_workspace_bytes(int64_t T, int32_t H)
+{
+    return (size_t)grad_blocks(T, H) * H * 4 + (H > kNormWide ? (size_t)T * 8 : 0);
+}
+
+hipError_t launch_rms_norm_backward(NormGradArgs p, bool fp32, bool accumulate, float *grad_weight, void *workspace,
+                                    hipStream_t stream)
+{
+    const int32_t blocks = grad_blocks(p.T, p.H);
+    p.partial = grad_weight ? static_cast<float *>(workspace) : nullptr;
+    p.stats = static_cast<float *>(workspace) + (size_t)blocks * p.H;
+    if (p.T > 0) {
+        const hipError_t err = fp32 ? norm_grad_by_width<true>(p, stream) : norm_grad_by_width<false>(p, stream);
+        if (err != hipSuccess || !grad_weight)
+            return err;
+    }
+    hipLaunchKernelGGL(rms_norm_join_kernel, dim3((unsigned)((p.H + kWave - 1) / kWave)), dim3(kJoinWaves * kWave), 0,
+                       stream, p.partial, blocks, p.H, accumulate, grad_weight);
+    return hipGetLastError();
+}
+
+}  // namespace moe

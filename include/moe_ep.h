@@ -755,6 +755,174 @@ moe_status_t moe_expert_product_wgrad(const uint16_t *grad_y, const uint16_t *x,
                                       void *grad_W, float *grad_bias, void *workspace,
                                       size_t workspace_bytes, void *stream);
 
+/* moe_rms_norm and moe_rms_norm_backward flags */
+#define MOE_NORM_FP32 1u         /* x, residual, total and their gradients are float32, else bf16 */
+#define MOE_NORM_WEIGHT_FP32 2u  /* weight is float32, else bf16 */
+#define MOE_NORM_ACCUMULATE 4u   /* backward: add to grad_weight */
+
+/*
+ * moe_rms_norm -- the norm in front of the layer, with the residual's
+ * addition:
+ *   total[t] = round(x[t] + residual[t])        (x[t] itself without residual)
+ *   v[t][h]  = total[t][h] * rsqrt(mean over h of total[t][h]^2 + eps) * weight[h]
+ *   y[t]     = bf16(v[t])                       where y is given
+ *   y8[t]    = v[t] as an FP8 row               where y8 is given
+ * The norm is of total as it is stored, so that the backward pass, which reads
+ * it, differentiates the function that ran. Sums and v are float32; y and y8
+ * are each one rounding of v. y is what the router reads, and y8 has the
+ * format of moe_dispatch_permute_fp8's rows (codes, scale bytes, zero padding):
+ * moe_dispatch_permute moves FP8 rows as bf16 rows of moe_fp8_row_bytes(H) / 2
+ * columns, and moe_expert_product_fp8 multiplies them. A value that is NaN or
+ * infinite becomes a NaN code; a row that holds one is NaN throughout.
+ *
+ * Defined by: ai-from-scratch "19. All-to-all", intro (every token's vector
+ * after attention enters the layer) and "MoE All-to-All Dispatch and Ragged
+ * Routing", "Returning Tokens to the Original GPU" (the residual stream);
+ * aicassindra "gpu_moe_all_to_all", "Latency-bound at decode, bandwidth-bound
+ * at prefill" (a lower-precision payload). The pages name no norm; this is the
+ * root-mean-square one.
+ *
+ * Arguments:
+ *   x         [T][H] bf16, or float32 with MOE_NORM_FP32.
+ *   residual  [T][H] as x, or NULL.
+ *   weight    [H] bf16, or float32 with MOE_NORM_WEIGHT_FP32.
+ *   eps       finite, >= 0.
+ *   total     [T][H] as x out; needed with residual, not accepted without it;
+ *             may be x or residual.
+ *   y         [T][H] bf16 out or NULL;  y8 [T][moe_fp8_row_bytes(H)] bytes out
+ *             or NULL; not both NULL. Neither may alias an input or total.
+ *   Buffers are 16-byte aligned.
+ * Limits: T < 2^31, H % 8 == 0 (H % 32 == 0 with y8), 0 < H <= 65536. A row's
+ *   sum of squares must lie within float32's range.
+ * Errors: MOE_ERR_INVALID_ARG (pointers, alignment, T < 0, eps, unknown flags),
+ *   MOE_ERR_UNSUPPORTED (limits).
+ */
+moe_status_t moe_rms_norm(const void *x, const void *residual, const void *weight, int64_t T,
+                          int32_t H, float eps, uint32_t flags, void *total, uint16_t *y,
+                          uint8_t *y8, void *stream);
+
+/*
+ * moe_rms_norm_backward -- the gradients of moe_rms_norm's v. With
+ * r = rsqrt(mean(total^2) + eps), recomputed from total, and g = grad_y * weight:
+ *   grad_x[t][h]   = r (g[h] - total[t][h] r^2 mean(g * total[t])) + grad_total[t][h]
+ *   grad_weight[h] = sum over t of grad_y[t][h] * total[t][h] * r
+ * grad_x is the gradient of x and of residual alike; grad_total is what
+ * reaches the residual stream from behind the layer. FP8 rows are
+ * differentiated as the values that they round (straight through). Every
+ * element of grad_weight is written (T = 0: zeros, or what it had with
+ * MOE_NORM_ACCUMULATE); the sum's order depends on T and H only.
+ *
+ * Arguments:
+ *   grad_y      [T][H] bf16.
+ *   total       [T][H] as moe_rms_norm stored it (x where it had no residual).
+ *   weight, eps, flags  as moe_rms_norm's, and MOE_NORM_ACCUMULATE.
+ *   grad_total  [T][H] as x, or NULL (zero).
+ *   grad_x      [T][H] as x out, or NULL; may be grad_total.
+ *   grad_weight [H] float32 out, or NULL (not both NULL).
+ *   workspace   moe_rms_norm_backward_workspace_size() bytes, 16-byte aligned,
+ *               contents on entry do not matter (NULL when the size is 0).
+ *               Calls that overlap in time must not share a workspace.
+ * Errors: as moe_rms_norm; MOE_ERR_WORKSPACE.
+ */
+moe_status_t moe_rms_norm_backward_workspace_size(int64_t T, int32_t H, size_t *bytes);
+moe_status_t moe_rms_norm_backward(const uint16_t *grad_y, const void *total, const void *weight,
+                                   int64_t T, int32_t H, float eps, uint32_t flags,
+                                   const void *grad_total, void *grad_x, float *grad_weight,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* moe_fp8_quantize_weights flags */
+#define MOE_WEIGHTS_FP32 1u  /* W is float32, else bf16 */
+
+/*
+ * moe_fp8_quantize_weights -- the experts' weights in 8 bits, with a float32
+ * scale for each block of 128 x 128 (smaller at the lower and right edges):
+ *   scale[l][a][b] = max|W[l]| in rows 128 a.. and columns 128 b.., over 448
+ *                    (1 for a block of zeros; at least 2^-126)
+ *   codes[l][o][h] = E4M3 nearest to W[l][o][h] * (1 / scale), ties to even
+ * and, where codes_t is given, both transposed, as the input gradient reads
+ * them: codes_t[l][h][o] = codes[l][o][h], scale_t[l][b][a] = scale[l][a][b].
+ * NaN and infinite weights get the NaN code; an infinity makes its block's
+ * scale infinite.
+ *
+ * Defined by: aicassindra "gpu_moe_all_to_all", "Latency-bound at decode,
+ * bandwidth-bound at prefill" (the expert matmul casts its input to a lower
+ * precision); the blocks are this library's reading.
+ *
+ * Arguments: W [n][O][H] bf16, or float32 with MOE_WEIGHTS_FP32; codes
+ *   [n][O][H] bytes, scale [n][ceil(O/128)][ceil(H/128)] float32 out; codes_t
+ *   [n][H][O] bytes and scale_t [n][ceil(H/128)][ceil(O/128)] float32 out, or
+ *   both NULL. W, codes and codes_t are 16-byte aligned. No output aliases W.
+ * Limits: 0 <= n <= 1024; O and H multiples of 32 in [32, 65536] (131072 for O,
+ *   the rows of a gated weight).
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED.
+ */
+moe_status_t moe_fp8_quantize_weights(const void *W, int32_t n, int32_t O, int32_t H,
+                                      uint32_t flags, uint8_t *codes, float *scale,
+                                      uint8_t *codes_t, float *scale_t, void *stream);
+
+/*
+ * moe_expert_product_fp8 -- moe_expert_product on FP8 rows and 8-bit weights:
+ *   z[i][o] = sum_h x[i][h] * W[l][o][h] + bias[l][o]
+ *     x[i][h]    = value(code) * 2^(scale byte - 127)     (row i, moe_fp8_dequant's value)
+ *     W[l][o][h] = value(W code[l][o][h]) * W_scale[l][o / 128][h / 128]
+ * with the bias, activation, gate and residual of moe_expert_product, and the
+ * result v to y (bf16), to y8 (FP8 rows of O values, the next product's input)
+ * or to both, each one rounding of the float32 v. The products of 128 values
+ * are summed on the matrix units, scaled rows times codes, then multiplied by
+ * the weights' scale and added in float32.
+ * A v that is NaN or infinite becomes a NaN code in y8.
+ *
+ * Defined by: as moe_expert_product, and aicassindra "gpu_moe_all_to_all",
+ * "Latency-bound at decode, bandwidth-bound at prefill" (the expert matmul in
+ * the payload's precision).
+ *
+ * Arguments: as moe_expert_product, but
+ *   x         [max_rows][moe_fp8_row_bytes(H)] bytes, as moe_dispatch_permute_fp8,
+ *             moe_rms_norm and this call write them.
+ *   W         [E_l][O][H] bytes ([E_l][2 O][H] gated), E4M3 codes.
+ *   W_scale   [E_l][ceil(O/128)][ceil(H/128)] float32 (gated: ceil(2 O/128); its
+ *             blocks run over all 2 O rows), 4-byte aligned.
+ *   y         [max_rows][O] bf16 out or NULL;  y8 [max_rows]
+ *             [moe_fp8_row_bytes(O)] bytes out or NULL; not both NULL. Rows
+ *             from expert_offsets[E_l] on are neither read nor written.
+ * Limits: as moe_expert_product, with H % 32 == 0 and O % 32 == 0. The rows'
+ *   sums over 128 values, before the weights' scale, must lie within
+ *   float32's range (rows below 2^100 do).
+ * Errors: as moe_expert_product.
+ */
+moe_status_t moe_expert_product_fp8(const uint8_t *x, const int32_t *expert_offsets, int32_t E_l,
+                                    int64_t max_rows, int32_t H, int32_t O, const uint8_t *W,
+                                    const float *W_scale, const uint16_t *bias,
+                                    const uint16_t *residual, int32_t act, uint32_t flags,
+                                    uint16_t *pre, uint16_t *y, uint8_t *y8, void *stream);
+
+/*
+ * moe_expert_product_fp8_dgrad -- moe_expert_product_dgrad on FP8 rows and the
+ * transposed 8-bit weights:
+ *   d[i][h] = sum_o grad_y[i][o] * W[l][o][h]
+ * through the activation as there, to grad_x (bf16, what the weights' gradient
+ * reads), to grad_x8 (FP8 rows, what the gradient of the product before it
+ * reads) or to both. The weights' gradient itself sums over rows, along which
+ * FP8 rows share no scale: it is moe_expert_product_wgrad on bf16 rows.
+ *
+ * Arguments: as moe_expert_product_dgrad, but
+ *   grad_y    [max_rows][moe_fp8_row_bytes(O)] bytes.
+ *   W_t       [E_l][H][O] bytes and W_t_scale [E_l][ceil(H/128)][ceil(O/128)]
+ *             float32: moe_fp8_quantize_weights' codes_t and scale_t (of a
+ *             gated product: H, and O = its 2 O rows).
+ *   grad_x    [max_rows][H] ([max_rows][2 H] gated) bf16 out or NULL; may be pre
+ *             itself.
+ *   grad_x8   [max_rows][moe_fp8_row_bytes(H)] (of 2 H gated) bytes out or NULL;
+ *             not both NULL.
+ * Limits: as moe_expert_product_fp8, and 2 H <= 65536 gated with grad_x8.
+ * Errors: as moe_expert_product_dgrad.
+ */
+moe_status_t moe_expert_product_fp8_dgrad(const uint8_t *grad_y, const int32_t *expert_offsets,
+                                          int32_t E_l, int64_t max_rows, int32_t O, int32_t H,
+                                          const uint8_t *W_t, const float *W_t_scale,
+                                          const uint16_t *pre, int32_t act, uint32_t flags,
+                                          uint16_t *grad_x, uint8_t *grad_x8, void *stream);
+
 /* moe_hbm_floor flags */
 #define MOE_FLOOR_NT_STORE 1u  /* stores carry the non-temporal hint */
 
