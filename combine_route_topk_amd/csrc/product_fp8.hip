@@ -15,145 +15,354 @@
 namespace moe {
 namespace {
 
-// the rows' scales of four K-tiles: 16 bytes for each of the tile's 256 rows
+// LDS: both stages of A, then both of B, so that one address register reaches
+// each operand's 64 KiB by instruction offsets; then two stages of the rows'
+// scales of four K-tiles, 16 bytes for each of the tile's 256 rows.
+constexpr int kStage8 = 2 * kHalfBytes, kB8 = 2 * kStage8, kScales8 = 2 * kB8;
 constexpr int kScaleStage = kTile * 16;
-// The scale bytes of a lane's row for a K-tile: of the 32 values numbered
-// lane / 16, for each of the eight groups of 16 rows of a wave.
-struct RowScales {
-    uint32_t v[2][4];
-};
-
-// The slot that reads the first half of A, and the K-tile's row scales.
-__device__ __forceinline__ void slot_a_scales(const FragAddr<false, 4> &fa, uint32_t stage, uint32_t scale, FragA &a,
-                                              RowScales &s)
+constexpr uint32_t kBehind = 0x40000000u;  // past the end of every operand of a tile, and no carry with `from`
+constexpr int kLds8 = kScales8 + 2 * kScaleStage;
+// A load of 16 bytes per lane into LDS, at `dst` and 16 bytes on for each lane.
+// It is written as an instruction (it has no register result) so that the
+// compiler does not know of it: it would wait for all such loads in flight
+// before every LDS read. The schedule below orders them with barriers and
+// counted waits instead. (M0 cannot be named as overwritten; nothing else in
+// these kernels uses it.)
+__device__ __forceinline__ void load_to_lds(uint32_t dst, u32x4 r, uint32_t off, uint32_t soff)
 {
-    asm volatile(MOE_READ_A(0, 1, 2, 3, 4, 5, 6, 7, 16, 17)
-                 "ds_read_u8 %8, %18\n\tds_read_u8 %9, %18 offset:256\n\t"
-                 "ds_read_u8 %10, %18 offset:512\n\tds_read_u8 %11, %18 offset:768\n\t"
-                 "ds_read_u8 %12, %18 offset:2048\n\tds_read_u8 %13, %18 offset:2304\n\t"
-                 "ds_read_u8 %14, %18 offset:2560\n\tds_read_u8 %15, %18 offset:2816\n\t" MOE_SLOT_END
-                 : MOE_OUT_A(a), "=&v"(s.v[0][0]), "=&v"(s.v[0][1]), "=&v"(s.v[0][2]), "=&v"(s.v[0][3]),
-                   "=&v"(s.v[1][0]), "=&v"(s.v[1][1]), "=&v"(s.v[1][2]), "=&v"(s.v[1][3])
-                 : "v"(stage + fa.a[0]), "v"(stage + fa.a[1]), "v"(scale), [half] "n"(0)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(dst), "v"(off), "s"(r), "s"(soff)
                  : "memory");
 }
 
-struct Gemm8 : Gemm<false, false> {
-    const uint8_t *scales;    // of the tile's first row
-    uint32_t scale_records, scale_row;
-    uint32_t scale_read;      // this lane's address in a stage of scales
+__device__ __forceinline__ u32x4 descriptor(const uint8_t *p, uint32_t records)
+{
+    const uint64_t at = (uint64_t)(uintptr_t)p;
+    return u32x4{(uint32_t)at, (uint32_t)(at >> 32), records, (uint32_t)kGemmBufferFlags};
+}
+
+template <class T>
+__device__ __forceinline__ T lds_read(uint32_t at)
+{
+    return *(__attribute__((address_space(3))) const T *)(uintptr_t)at;
+}
+
+// Fragments of A (four of 16 rows) and B (two of 16 columns): 128 k of a row in
+// four lanes, a lane's 32 in two pieces of 16 that lie 64 apart.
+struct FragA8 {
+    i32x8 v[4];
+    uint32_t s[4];  // scale bytes of the lane's row, for its 32 of the K-tile's values
+};
+struct FragB8 {
+    i32x8 v[2];
+};
+__device__ __forceinline__ i32x8 read_frag(uint32_t at0, uint32_t at1)
+{
+    const i32x4 lo = lds_read<i32x4>(at0), hi = lds_read<i32x4>(at1);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// A block's scale s of the weights as the product of the power of two that the
+// MFMA multiplies by, and of a factor of magnitude [1, 2). Accumulators are kept
+// in units of the factor: they are multiplied by the old one over the new where
+// it changes, which is between 1/2 and 2 whatever the scales are. A scale below
+// 2^-126 counts as 2^-127; one that is infinite or NaN gives NaN.
+struct Scale8 {
+    uint32_t power;  // E8M0
+    float factor;
+};
+__device__ __forceinline__ Scale8 split(float s)
+{
+    const uint32_t bits = __float_as_uint(s), power = (bits >> 23) & 255;
+    return {power, __uint_as_float(power ? (bits & 0x807FFFFFu) | 0x3F800000u : 0x3F800000u)};
+}
+
+// An operand of a tile, as Operand<false>, with one offset per lane: the loads of
+// other rows lie a uniform distance from it, which is part of the scalar offset.
+// The descriptor's end is checked less the scalar offset, which must not pass
+// it: where it would, it is the end itself, and every lane gets zeros.
+struct Operand8 {
+    u32x4 r;
+    uint32_t off;
+    uint32_t from[2][2];  // of load i of half h
+
+    // `rows` valid rows (one or more), ld bytes apart; `row`: of this wave's load 0 of half 0
+    __device__ __forceinline__ void init(const uint8_t *p, int32_t rows, int32_t ld, int lane, int row, int half_rows,
+                                         int second_rows)
+    {
+        // the same in every lane, which the compiler cannot always tell
+        r = descriptor(p, __builtin_amdgcn_readfirstlane((uint32_t)(min(rows, kTile) * ld)));
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            r[i] = __builtin_amdgcn_readfirstlane(r[i]);
+        off = (uint32_t)(row + (lane >> 3)) * (uint32_t)ld + ((lane & 7) ^ (lane >> 3)) * 16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                from[h][i] = (uint32_t)((h * half_rows + i * second_rows) * ld);
+    }
+    // Start the two loads of half H of the K-tile at byte k0 of the rows
+    // (kBehind for one behind the last: zeros) into LDS at dst + AT and 8 KiB on.
+    // One block of instructions, so that the reading slot has few.
+    template <int H, int AT>
+    __device__ __forceinline__ void load(uint32_t dst, uint32_t k0) const
+    {
+        uint32_t x, y;
+        asm volatile("s_add_u32 %[x], %[f0], %[k0]\n\ts_add_u32 m0, %[dst], %[at0]\n\ts_min_u32 %[x], %[x], %[end]\n\t"
+                     "buffer_load_dwordx4 %[v], %[r], %[x] offen lds\n\t"
+                     "s_add_u32 %[y], %[f1], %[k0]\n\ts_add_u32 m0, %[dst], %[at1]\n\ts_min_u32 %[y], %[y], %[end]\n\t"
+                     "buffer_load_dwordx4 %[v], %[r], %[y] offen lds"
+                     : [x] "=&s"(x), [y] "=&s"(y)
+                     : [f0] "s"(from[H][0]), [f1] "s"(from[H][1]), [k0] "s"(k0), [dst] "s"(dst), [at0] "n"(AT),
+                       [at1] "n"(AT + 8192), [end] "s"(r[2]), [v] "v"(off), [r] "s"(r)
+                     : "memory", "scc");
+    }
+};
+
+// The K loop of one 256 x 256 tile. Schedule as in product_gemm.hpp: phases of
+// 8 MFMAs, and waves 0-3 half a phase apart from waves 4-7, so that one of a
+// SIMD's two waves reads while the other multiplies. An MFMA holds its SIMD's
+// vector issue for 16 of its 32 cycles and its own wave for longer (FMAs
+// between a wave's MFMAs delayed each by all of their time), so the FMAs with
+// the weights' scale are the reading wave's: it starts its reads, then adds the
+// results of its last phase to the accumulators, then waits.
+struct Gemm8 {
+    Operand8 a8, b8;
+    uint32_t lds, lds_wave;   // LDS, and where this wave's loads begin in it
+    uint32_t tail;
+    uint32_t fa[2], fb[2];    // LDS addresses of this lane's pieces of a fragment: 16 k of the first 64, and of the second
+    u32x4 scales;             // descriptor of the tile's row scales
+    uint32_t scale_row;       // this lane's row among them when it loads
+    uint32_t scale_read;      // and its address in a stage of scales when it reads
     int32_t last_scales;      // scale bytes of the last K-tile, 1 to 4
     const float *ws[2];       // the weights' scales of this wave's columns (gated: gate, up), one for each K-tile
+    int wave, lane, wm, wn;
+    uint32_t low, high;       // whether this wave's rows of A's first and second half are among the tile's
 
-    __device__ __forceinline__ void init_scales(const uint8_t *rows_, int32_t rows, int32_t K, int64_t row_bytes)
+    __device__ __forceinline__ void init_lane(uint32_t lds_)
     {
-        scales = rows_ + K;
-        scale_records = (uint32_t)(rows * row_bytes - K);
+        lds = lds_;
+        lane = threadIdx.x & (kWave - 1);
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        lds_wave = lds + wave * 1024;
+        wm = wave >> 2;
+        wn = wave & 3;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            fa[kk] = lds + frag_row(wm * 64, kk, lane);
+            fb[kk] = lds + kB8 + frag_row(wn * 32, kk, lane);
+        }
+    }
+    __device__ __forceinline__ void set_rows(int32_t rows)
+    {
+        low = __builtin_amdgcn_readfirstlane(rows > wm * 64);
+        high = __builtin_amdgcn_readfirstlane(rows > 128 + wm * 64);
+    }
+    // first of the 32 columns that acc[.][hB] holds for this wave
+    __device__ __forceinline__ int column(int hB) const { return wn * 64 + hB * 32; }
+
+    __device__ __forceinline__ void init_scales(const uint8_t *p, int32_t rows, int32_t K, int64_t row_bytes)
+    {
+        tail = K % kTileK8 && ((lane & 7) ^ (lane >> 3)) * 16 >= K % kTileK8 ? kOutside : 0u;
+        scales = descriptor(p + K, (uint32_t)(rows * row_bytes - K));
         scale_row = (uint32_t)(wave * kWave + lane) * (uint32_t)row_bytes;
-        scale_read = (uint32_t)((wm * 64 + (lane & 15)) * 16 + (lane >> 4));
+        scale_read = lds + kScales8 + (uint32_t)((wm * 64 + (lane & 15)) * 16 + (lane >> 4));
         last_scales = (K - 1) % kTileK8 / 32 + 1;
     }
-
     // start the load of the scales of K-tiles 4 q to 4 q + 3: waves 0 to 3, 64 rows each
-    __device__ __forceinline__ void load_scales(uint8_t *stages, int q) const
+    __device__ __forceinline__ void load_scales(int q) const
     {
         if (wave < 4)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(scales), 0, scale_records, kGemmBufferFlags),
-                stages + (q & 1) * kScaleStage + wave * (kWave * 16), 16, scale_row + q * 16, 0, 0, 0);
+            load_to_lds(lds + kScales8 + (q & 1) * kScaleStage + wave * (kWave * 16), scales, scale_row, q * 16);
+    }
+    template <int S, int H>
+    __device__ __forceinline__ void load_a(uint32_t k0) const
+    {
+        a8.load<H, S * kStage8 + H * kHalfBytes>(lds_wave, k0);
+    }
+    template <int S, int H>
+    __device__ __forceinline__ void load_b(uint32_t k0) const
+    {
+        b8.load<H, kB8 + S * kStage8 + H * kHalfBytes>(lds_wave, k0);
+    }
+    // from the last K-tile on, pieces past K read as zeros
+    __device__ __forceinline__ void cut_tail()
+    {
+        a8.off |= tail;
+        b8.off |= tail;
+    }
+    __device__ __forceinline__ static uint32_t k_of(int t, int nk) { return t < nk ? (uint32_t)t * kTileK8 : kBehind; }
+
+    // the loads that run ahead of the first phase, in the order they are waited for
+    __device__ __forceinline__ void start(int nk)
+    {
+        load_scales(0);
+        if (nk == 1)
+            cut_tail();
+        load_b<0, 0>(0);
+        load_a<0, 0>(0);
+        load_b<0, 1>(0);
+        load_a<0, 1>(0);
+        // K-tile 1's second half of A follows in the loop: its tail is cut there
+        const uint32_t k1 = k_of(1, nk);
+        if (nk == 2)
+            cut_tail();
+        load_b<1, 0>(k1);
+        load_a<1, 0>(k1);
+        load_b<1, 1>(k1);
     }
 
-    // c += w * (a b), w[j] for column group j
-    __device__ __forceinline__ static void mfmas8(const FragA &a, const FragB &b, const uint32_t (&s)[4],
-                                                  const float (&w)[2], f32x4 (&c)[4][2])
+    // `at`: of the half tile, among its operand's
+    __device__ __forceinline__ void read_a(int at, uint32_t scale, FragA8 &a) const
     {
-        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            a.v[i] = read_frag(fa[0] + (at + i * 2048), fa[1] + (at + i * 2048));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            a.s[i] = lds_read<uint8_t>(scale + i * 256);
+    }
+    __device__ __forceinline__ void read_b(int at, FragB8 &b) const
+    {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            b.v[j] = read_frag(fb[0] + (at + j * 2048), fb[1] + (at + j * 2048));
+    }
+
+    // c += a b times the weights' powers of two, w[j] for column group j
+    __device__ __forceinline__ static void multiply(const FragA8 &a, const FragB8 &b, const Scale8 (&w)[2],
+                                                    f32x4 (&c)[4][2])
+    {
         __builtin_amdgcn_s_setprio(1);
-        f32x4 p[4][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                p[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    join8(b.v[0][j], b.v[1][j]), join8(a.v[0][i], a.v[1][i]), f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, kOne, 0,
-                    s[i]);
+                c[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v[j], a.v[i], c[i][j], 0, 0, 0, w[j].power, 0,
+                                                                           a.s[i]);
+        __builtin_amdgcn_s_setprio(0);
+    }
+    // accumulators from the units of the K-tile before to this one's
+    __device__ __forceinline__ static void rescale(const float (&r)[2], f32x4 (&c)[4][2])
+    {
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    c[i][j][e] = fmaf(w[j], p[i][j][e], c[i][j][e]);
-        __builtin_amdgcn_s_setprio(0);
+                    c[i][j][e] *= r[j];
     }
 
-    // As Gemm::ktile. The scales that replace a stage are started two slots
-    // after every wave's reads of its last K-tile.
-    __device__ __forceinline__ void ktile8(uint8_t *cur, uint8_t *other, uint8_t *stages, int t, int nk, const FragB &b0,
-                                           FragB &next, const float (&w)[2], float (&wn_)[2], Acc &acc) const
+    // The end of a reading slot: the loads that the next phase reads have
+    // arrived, for every wave behind the barrier, and so have this wave's reads.
+    // (What reads into LDS replaces is so read to its end one barrier before.)
+    __device__ __forceinline__ static void reads_end()
     {
-        const uint32_t at = lds_offset(cur), then = lds_offset(other);
-        FragA a;
-        FragB b1;
-        RowScales s;
-        const int tn = min(t + 1, nk - 1);
-        wn_[0] = load_uniform(ws[0] + tn);
-        wn_[1] = load_uniform(ws[1] + tn);
-        A.load(other + kHalfBytes, 1, t + 1, nk, wave);
-        uint32_t from = lds_offset(stages) + ((t >> 2) & 1) * kScaleStage + (t & 3) * 4 + scale_read;
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(10)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_s_waitcnt((63 & 15) | ((63 >> 4) << 14) | (7 << 4));  // lgkmcnt(0); the compiler counts along
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __device__ __forceinline__ static void products_end()
+    {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // K-tile t, which lies in stage S; b0 holds its first half of B, and next
+    // receives the next K-tile's. w holds its scales and receives the next
+    // K-tile's, r takes the accumulators to its units and receives the next's.
+    template <int S>
+    __device__ __forceinline__ void ktile(int t, int nk, const FragB8 &b0, FragB8 &next, Scale8 (&w)[2], float (&r)[2],
+                                          Acc &acc)
+    {
+        FragA8 a;
+        FragB8 b1;
+        uint32_t from = scale_read + (((t >> 2) & 1) * kScaleStage + (t & 3) * 4);
         if (t == nk - 1)  // past K zeros meet the last scale that is one, not what lies behind it
             from -= max((lane >> 4) + 1 - last_scales, 0);
-        slot_a_scales(fa, at, from, a, s);
+        const int tn = min(t + 1, nk - 1);
+        const uint32_t k1 = k_of(t + 1, nk), k2 = k_of(t + 2, nk);
+        load_a<1 - S, 1>(k1);
+        if (t + 3 == nk)
+            cut_tail();
+        read_a(S * kStage8, from, a);
+        rescale(r, acc[0][0]);
+        reads_end();
         if (low)
-            mfmas8(a, b0, s.v[0], w, acc[0][0]);
-        slot_end();
-        B.load(cur + 2 * kHalfBytes, 0, t + 2, nk, wave);
-        slot_b<3>(fb, at, b1);
+            multiply(a, b0, w, acc[0][0]);
+        products_end();
+        load_b<S, 0>(k2);
+        read_b(S * kStage8 + kHalfBytes, b1);
+        rescale(r, acc[0][1]);
+        reads_end();
         if (low)
-            mfmas8(a, b1, s.v[0], w, acc[0][1]);
-        slot_end();
-        A.load(cur, 0, t + 2, nk, wave);
-        if ((t & 3) == 0 && t + 4 < nk)
-            load_scales(stages, (t >> 2) + 1);
-        if (high) {
-            slot_a<1>(fa, at, a);
-            mfmas8(a, b1, s.v[1], w, acc[1][1]);
-        } else {
-            wait_loads<10>();
-            slot_end();
-        }
-        slot_end();
-        B.load(cur + 3 * kHalfBytes, 1, t + 2, nk, wave);
-        slot_b<2>(fb, then, next);
+            multiply(a, b1, w, acc[0][1]);
+        products_end();
+        load_a<S, 0>(k2);
+        if ((t & 3) == 0 && t + 4 < nk)  // two slots after every wave's last reads of the stage
+            load_scales((t >> 2) + 1);
+        read_a(S * kStage8 + kHalfBytes, from + 128 * 16, a);
+        rescale(r, acc[1][1]);
+        reads_end();
         if (high)
-            mfmas8(a, b0, s.v[1], w, acc[1][0]);
-        slot_end();
+            multiply(a, b1, w, acc[1][1]);
+        __builtin_amdgcn_sched_barrier(0);
+        // nothing waits for LDS before these are needed, which would wait for them too
+        const float s0 = load_uniform(ws[0] + tn), s1 = load_uniform(ws[1] + tn);
+        products_end();
+        load_b<S, 1>(k2);
+        read_b((1 - S) * kStage8, next);
+        rescale(r, acc[1][0]);
+        reads_end();
+        if (high)
+            multiply(a, b0, w, acc[1][0]);
+        products_end();
+        const Scale8 n[2] = {split(s0), split(s1)};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            r[j] = w[j].factor * __builtin_amdgcn_rcpf(n[j].factor);
+            w[j] = n[j];
+            asm volatile("" : "+v"(w[j].power));  // the MFMA takes it from a vector register
+        }
     }
 
-    __device__ __forceinline__ void run8(uint8_t *lds, int nk, Acc &acc) const
+    // The whole K loop; start() has been called. On return every wave has read
+    // what it needs of LDS, and the loads still in flight bring only zeros.
+    __device__ __forceinline__ void run(int nk, Acc &acc)
     {
 #pragma unroll
         for (int q = 0; q < 16; ++q)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 acc[q >> 3][(q >> 2) & 1][q & 3][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        uint8_t *s0 = lds, *s1 = lds + kStageBytes, *stages = lds + kGemmLdsBytes;
-        float w0[2] = {load_uniform(ws[0]), load_uniform(ws[1])}, w1[2];
-        wait_loads<10>();
-        slot_end();
-        FragB b0, b1;
-        slot_b<2>(fb, lds_offset(s0), b0);
+        Scale8 w[2] = {split(load_uniform(ws[0])), split(load_uniform(ws[1]))};
+        float r[2] = {1.f, 1.f};
+        FragB8 b0, b1;
+        reads_end();
+        read_b(0, b0);
+        reads_end();
         if (wm)  // the second group of waves starts half a phase later
-            slot_end();
+            products_end();
         int t = 0;
         for (; t + 1 < nk; t += 2) {
-            ktile8(s0, s1, stages, t, nk, b0, b1, w0, w1, acc);
-            ktile8(s1, s0, stages, t + 1, nk, b1, b0, w1, w0, acc);
+            ktile<0>(t, nk, b0, b1, w, r, acc);
+            ktile<1>(t + 1, nk, b1, b0, w, r, acc);
         }
         if (t < nk)
-            ktile8(s0, s1, stages, t, nk, b0, b1, w0, w1, acc);
+            ktile<0>(t, nk, b0, b1, w, r, acc);
         if (!wm)
-            slot_end();
+            products_end();
+        // w holds the last K-tile's scales again
+        const float f[2] = {w[0].factor, w[1].factor};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            rescale(f, acc[q >> 1][q & 1]);
     }
 };
 
@@ -162,7 +371,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_fp8_kernel(Product8Ar
 {
     constexpr bool PAIR = GATED && !GRAD;
     constexpr int kCols = PAIR ? kTile / 2 : kTile;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kGemmLdsBytes + 2 * kScaleStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds8];
     __shared__ int32_t first[kMaxLocalExperts + 1];
     const int32_t row_tiles = plan_row_tiles<kGemmThreads, kTile>(p.off, p.El, p.max_rows, first);
     const uint32_t nct = (uint32_t)(p.N + kCols - 1) / kCols;
@@ -170,7 +379,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_fp8_kernel(Product8Ar
     const int nk = (p.K + kTileK8 - 1) / kTileK8;
     const int64_t nbw = (wide + 127) / 128;
     Gemm8 gemm;
-    gemm.init_lane();
+    gemm.init_lane(lds_offset(lds));
     // tiles and the slices of a last round as in product.hip
     const uint32_t slot = gridDim.x % 8 ? blockIdx.x : blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
     const uint32_t tiles = row_tiles * nct, rest = tiles % gridDim.x, whole = tiles - rest;
@@ -189,30 +398,28 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_fp8_kernel(Product8Ar
         const int32_t row0 = __builtin_amdgcn_readfirstlane((int32_t)at);
         const int32_t rows = __builtin_amdgcn_readfirstlane((int32_t)min((int64_t)most, r.end - at));
         const uint8_t *a = p.a + row0 * p.a_bytes;
-        const uint16_t *Wl = reinterpret_cast<const uint16_t *>(p.W + l * wide * p.K);  // in pairs of codes, as below
-        const int32_t K2 = p.K / 2;
-        gemm.A.init(reinterpret_cast<const uint16_t *>(a), rows, K2, (int32_t)(p.a_bytes / 2), gemm.wave, gemm.lane, 128,
-                    [](int j) { return j * 8; });
+        const uint8_t *Wl = p.W + l * wide * p.K;
+        gemm.a8.init(a, rows, (int32_t)p.a_bytes, gemm.lane, gemm.wave * 8, 128, 64);
         gemm.init_scales(a, rows, p.K, p.a_bytes);
         const float *ws = p.scale + l * nbw * nk;
-        // columns past the last have no scale of their own: theirs multiplies zeros
+        // Rows of B's halves as in product.hip, eight of a wave's load at a time.
+        // Columns past the last have no scale of their own: theirs multiplies zeros.
         if constexpr (PAIR) {
             const bool up = (gemm.wave >> 1) & 1;
-            gemm.B.init(Wl + ((up ? (int64_t)p.N : 0) + n0) * K2, p.N - n0, K2, K2, gemm.wave, gemm.lane, 16,
-                        [](int j) { return (j >> 2) * 32 + (j & 1) * 8; });
+            gemm.b8.init(Wl + ((up ? (int64_t)p.N : 0) + n0) * p.K, p.N - n0, p.K, gemm.lane,
+                         (gemm.wave >> 2) * 32 + (gemm.wave & 1) * 8, 16, 64);
             const int64_t c = min(n0 + gemm.wn * 32, p.N - 32);
             gemm.ws[0] = ws + c / 128 * nk;
             gemm.ws[1] = ws + (p.N + c) / 128 * nk;
         } else {
-            gemm.B.init(Wl + (int64_t)n0 * K2, p.N - n0, K2, K2, gemm.wave, gemm.lane, 32,
-                        [](int j) { return (j >> 2) * 64 + (j & 3) * 8; });
+            gemm.b8.init(Wl + (int64_t)n0 * p.K, p.N - n0, p.K, gemm.lane, (gemm.wave >> 2) * 64 + (gemm.wave & 3) * 8, 32,
+                         128);
             gemm.ws[0] = gemm.ws[1] = ws + min((int64_t)(n0 + gemm.wn * 64) / 128, nbw - 1) * nk;
         }
         Acc acc;
         gemm.set_rows(rows);
-        gemm.load_scales(lds + kGemmLdsBytes, 0);
-        gemm.start(lds, nk);
-        gemm.run8(lds, nk, acc);
+        gemm.start(nk);
+        gemm.run(nk, acc);
         epilogue<GRAD, GATED, ACT, true>(p, gemm, acc, l, row0, rows, n0);
         const int32_t width = GATED && GRAD ? 2 * p.N : p.N;
         if (p.out8 && n0 + kCols >= p.N)
