@@ -719,6 +719,13 @@ def moe_expert_product_wgrad(grad_y: torch.Tensor, x: torch.Tensor, expert_offse
 
 
 _U8 = (torch.uint8,)
+
+
+def _row8(H: int) -> int:
+    """moe_fp8_row_bytes of a width that the call itself checks, without a call."""
+    return H + 128 * ((H + 4095) // 4096)
+
+
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 
 
@@ -741,9 +748,9 @@ def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
         if need_y and y is None:
             y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
         if fp8 and y8 is None:
-            y8 = torch.empty((T, moe_fp8_row_bytes(H)), dtype=torch.uint8, device=dev)
+            y8 = torch.empty((T, _row8(H)), dtype=torch.uint8, device=dev)
         y = y if need_y else None
-        row = (T, moe_fp8_row_bytes(H)) if y8 is not None else None
+        row = (T, _row8(H)) if y8 is not None else None
         _check("moe_rms_norm", lib.moe_rms_norm(
             _ptr(x, _STREAM, "x", 2), _shaped(residual, "residual", (T, H), (dt,), dev),
             _shaped(weight, "weight", (H,), _STREAM, dev), T, H, eps,
@@ -840,15 +847,15 @@ def moe_expert_product_fp8(x: torch.Tensor, expert_offsets: torch.Tensor, W: tor
     if gated and wide % 2:
         raise ValueError("a gated W holds gate and up outputs in equal number")
     O = wide // 2 if gated else wide
-    if row != moe_fp8_row_bytes(H):
-        raise ValueError(f"x must be [n, {moe_fp8_row_bytes(H)}] bytes, got {list(x.shape)}")
+    if row != _row8(H):
+        raise ValueError(f"x must be [n, {_row8(H)}] bytes, got {list(x.shape)}")
     with _on(dev, stream):
         if need_y and y is None:
             y = torch.empty((max_rows, O), dtype=torch.bfloat16, device=dev)
         if fp8 and y8 is None:
-            y8 = torch.empty((max_rows, moe_fp8_row_bytes(O)), dtype=torch.uint8, device=dev)
+            y8 = torch.empty((max_rows, _row8(O)), dtype=torch.uint8, device=dev)
         y = y if need_y else None
-        row8 = (max_rows, moe_fp8_row_bytes(O)) if y8 is not None else None
+        row8 = (max_rows, _row8(O)) if y8 is not None else None
         _check("moe_expert_product_fp8", lib.moe_expert_product_fp8(
             _ptr(x, _U8, "x", 2), _shaped(expert_offsets, "expert_offsets", (El + 1,), _I32, dev), El, max_rows, H, O,
             _shaped(W, "W", (El, wide, H), _E4M3, dev),
@@ -874,15 +881,15 @@ def moe_expert_product_fp8_dgrad(grad_y: torch.Tensor, expert_offsets: torch.Ten
     dev = grad_y.device
     El, H, O = _need(W_t, "W_t", 3).shape
     wide = 2 * H if gated else H
-    if row != moe_fp8_row_bytes(O):
-        raise ValueError(f"grad_y must be [n, {moe_fp8_row_bytes(O)}] bytes, got {list(grad_y.shape)}")
+    if row != _row8(O):
+        raise ValueError(f"grad_y must be [n, {_row8(O)}] bytes, got {list(grad_y.shape)}")
     with _on(dev, stream):
         if need_x and grad_x is None:
             grad_x = torch.empty((max_rows, wide), dtype=torch.bfloat16, device=dev)
         if fp8 and grad_x8 is None:
-            grad_x8 = torch.empty((max_rows, moe_fp8_row_bytes(wide)), dtype=torch.uint8, device=dev)
+            grad_x8 = torch.empty((max_rows, _row8(wide)), dtype=torch.uint8, device=dev)
         grad_x = grad_x if need_x else None
-        row8 = (max_rows, moe_fp8_row_bytes(wide)) if grad_x8 is not None else None
+        row8 = (max_rows, _row8(wide)) if grad_x8 is not None else None
         _check("moe_expert_product_fp8_dgrad", lib.moe_expert_product_fp8_dgrad(
             _ptr(grad_y, _U8, "grad_y", 2), _shaped(expert_offsets, "expert_offsets", (El + 1,), _I32, dev), El,
             max_rows, O, H, _shaped(W_t, "W_t", (El, H, O), _E4M3, dev),

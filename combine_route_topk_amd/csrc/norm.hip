@@ -33,19 +33,28 @@ __device__ __forceinline__ float wave_sum(float v)
 template <bool FP32>
 struct Raw8 {
     u32x4 q[FP32 ? 2 : 1];
+    // rows, each once: past the caches (105 against 113 us, 32768 x 2048 forward)
     __device__ __forceinline__ void load(const void *p, int64_t chunk)
+    {
+        const u32x4 *s = static_cast<const u32x4 *>(p) + chunk * (FP32 ? 2 : 1);
+        q[0] = load_stream(s);
+        if (FP32)
+            q[FP32 ? 1 : 0] = load_stream(s + 1);
+    }
+    __device__ __forceinline__ void store(void *p, int64_t chunk) const
+    {
+        u32x4 *s = static_cast<u32x4 *>(p) + chunk * (FP32 ? 2 : 1);
+        store_stream(s, q[0]);
+        if (FP32)
+            store_stream(s + 1, q[FP32 ? 1 : 0]);
+    }
+    // the weight, for every row
+    __device__ __forceinline__ void load_cached(const void *p, int64_t chunk)
     {
         const u32x4 *s = static_cast<const u32x4 *>(p) + chunk * (FP32 ? 2 : 1);
         q[0] = s[0];
         if (FP32)
             q[FP32 ? 1 : 0] = s[1];
-    }
-    __device__ __forceinline__ void store(void *p, int64_t chunk) const
-    {
-        u32x4 *s = static_cast<u32x4 *>(p) + chunk * (FP32 ? 2 : 1);
-        s[0] = q[0];
-        if (FP32)
-            s[1] = q[FP32 ? 1 : 0];
     }
     __device__ __forceinline__ float get(int i) const
     {
@@ -61,34 +70,17 @@ struct Raw8 {
     }
 };
 
-// The weight's type is a branch, the same for every lane.
-__device__ __forceinline__ void load_weight(const void *w, bool fp32, int64_t chunk, float (&v)[8])
-{
-    if (fp32) {
-        Raw8<true> r;
-        r.load(w, chunk);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = r.get(i);
-    } else {
-        Raw8<false> r;
-        r.load(w, chunk);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = r.get(i);
-    }
-}
-
 // WPR waves take a row, each lane CH chunks of eight columns; a block of at
 // least four waves.
 constexpr int norm_threads(int wpr) { return wpr < 4 ? 256 : wpr * kWave; }
 constexpr int kScaleLine = 128;  // scale bytes of 4096 values
 
-template <bool FP32, int WPR, int CH>
+template <bool FP32, bool WFP32, int WPR, int CH>
 __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_kernel(NormArgs p)
 {
     constexpr int kRows = norm_threads(WPR) / kWave / WPR;
     constexpr int kLines = (WPR * CH * 512 + 4095) / 4096;
+    constexpr bool kEarly = CH <= 4;  // wider rows need the registers
     __shared__ float part[2][kRows][WPR];
     __shared__ __attribute__((aligned(16))) uint8_t scales[kRows][kLines * kScaleLine];
     const int lane = threadIdx.x & (kWave - 1);
@@ -106,12 +98,16 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_kernel(NormArgs p)
         const int64_t t = t0 + slot;
         const bool valid = t < p.T;
         Raw8<FP32> h[CH];
+        Raw8<WFP32> w[CH];
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int32_t c = (i * WPR + wr) * kWave + lane;
-            if (valid && c < C)
+            if (valid && c < C) {
                 h[i].load(p.x, t * C + c);
+                if (kEarly)
+                    w[i].load_cached(p.weight, c);
+            }
         }
         if (p.residual) {
             Raw8<FP32> r[CH];
@@ -159,12 +155,12 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_kernel(NormArgs p)
             const int32_t c = (i * WPR + wr) * kWave + lane;
             if (!valid || c >= C)
                 continue;
-            float v[8];
-            load_weight(p.weight, p.weight_fp32, c, v);
-            float m = 0.f;
+            if (!kEarly)
+                w[i].load_cached(p.weight, c);
+            float v[8], m = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                v[e] *= h[i].get(e) * r;
+                v[e] = h[i].get(e) * r * w[i].get(e);
                 m = max_abs(m, v[e]);
             }
             if (p.y) {
@@ -179,7 +175,7 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_kernel(NormArgs p)
                 const int32_t e = fp8_exponent(m);
                 const float mul = fp8_multiplier(e);
                 const u32x2 codes = {fp8_encode4(v[0], v[1], v[2], v[3], mul), fp8_encode4(v[4], v[5], v[6], v[7], mul)};
-                reinterpret_cast<u32x2 *>(p.y8 + t * p.y8_bytes)[c] = codes;
+                __builtin_nontemporal_store(codes, reinterpret_cast<u32x2 *>(p.y8 + t * p.y8_bytes) + c);
                 if ((lane & 3) == 0)
                     scales[slot][c >> 2] = (uint8_t)(e + 127);
             }
@@ -191,7 +187,8 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_kernel(NormArgs p)
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             const int i = wr * kWave + lane;  // the row's scale bytes in whole lines
             if (valid && i < pad / 16)
-                reinterpret_cast<u32x4 *>(p.y8 + t * p.y8_bytes + p.H)[i] = reinterpret_cast<const u32x4 *>(scales[slot])[i];
+                store_stream(reinterpret_cast<u32x4 *>(p.y8 + t * p.y8_bytes + p.H) + i,
+                             reinterpret_cast<const u32x4 *>(scales[slot])[i]);
             if (WPR > 1)
                 __syncthreads();
             else
@@ -208,7 +205,7 @@ struct RowStats {
 // The gradient of rows blockIdx.x * kRows + slot, and further ones, in columns
 // from blockIdx.y * (the columns that the waves cover). GIVEN: the row's
 // statistics are read from p.stats, since a block covers only a part of the row.
-template <bool FP32, int WPR, int CH, bool GIVEN>
+template <bool FP32, bool WFP32, int WPR, int CH, bool GIVEN>
 __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_backward_kernel(NormGradArgs p)
 {
     constexpr int kRows = norm_threads(WPR) / kWave / WPR;
@@ -219,16 +216,21 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_backward_kernel(No
     const int slot = wave / WPR, wr = wave % WPR;
     const int32_t C = p.H / 8, c0 = GIVEN ? blockIdx.y * (WPR * CH * kWave) : 0;
     float acc[CH][8];
+    Raw8<WFP32> w[CH];
 #pragma unroll
-    for (int i = 0; i < CH; ++i)
+    for (int i = 0; i < CH; ++i) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             acc[i][e] = 0.f;
+        const int32_t c = c0 + (i * WPR + wr) * kWave + lane;
+        if (c < C)
+            w[i].load_cached(p.weight, c);
+    }
     int parity = 0;
     for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += (int64_t)gridDim.x * kRows) {
         const int64_t t = t0 + slot;
         const bool valid = t < p.T;
-        Raw8<FP32> h[CH];
+        Raw8<FP32> h[CH], d[CH];
         Raw8<false> g[CH];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
@@ -236,8 +238,14 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_backward_kernel(No
             if (valid && c < C) {
                 h[i].load(p.t, t * C + c);
                 g[i].load(p.grad_y, t * C + c);
+                if (p.grad_x && p.grad_total)
+                    d[i].load(p.grad_total, t * C + c);
             }
         }
+        if (!WFP32)  // kept as it lies in memory: widened ahead of the loop it would take twice the registers
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+                asm volatile("" : "+v"(w[i].q[0]));
         RowStats s = {0.f, 0.f};
         if (GIVEN) {
             if (valid)
@@ -247,15 +255,12 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_backward_kernel(No
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 const int32_t c = c0 + (i * WPR + wr) * kWave + lane;
-                if (valid && c < C) {
-                    float w[8];
-                    load_weight(p.weight, p.weight_fp32, c, w);
+                if (valid && c < C)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         s0 = fmaf(h[i].get(e), h[i].get(e), s0);
-                        s1 = fmaf(g[i].get(e) * w[e], h[i].get(e), s1);
+                        s1 = fmaf(g[i].get(e) * w[i].get(e), h[i].get(e), s1);
                     }
-                }
             }
             s0 = wave_sum(s0);
             s1 = wave_sum(s1);
@@ -283,18 +288,14 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_backward_kernel(No
             if (!valid || c >= C)
                 continue;
             if (p.grad_x) {
-                float w[8], v[8];
-                load_weight(p.weight, p.weight_fp32, c, w);
+                float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    v[e] = s.r * (g[i].get(e) * w[e] - h[i].get(e) * s.c);
-                if (p.grad_total) {
-                    Raw8<FP32> d;
-                    d.load(p.grad_total, t * C + c);
+                    v[e] = s.r * (g[i].get(e) * w[i].get(e) - h[i].get(e) * s.c);
+                if (p.grad_total)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        v[e] += d.get(e);
-                }
+                        v[e] += d[i].get(e);
                 Raw8<FP32> o;
                 o.set(v);
                 o.store(p.grad_x, t * C + c);
@@ -341,7 +342,7 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_backward_kernel(No
 
 // Statistics of rows too wide for one block's registers: a block per row.
 constexpr int kStatThreads = 512;
-template <bool FP32>
+template <bool FP32, bool WFP32>
 __global__ __launch_bounds__(kStatThreads) void rms_norm_stats_kernel(NormGradArgs p)
 {
     __shared__ float part[2][kStatThreads / kWave];
@@ -352,14 +353,14 @@ __global__ __launch_bounds__(kStatThreads) void rms_norm_stats_kernel(NormGradAr
         for (int32_t c = threadIdx.x; c < C; c += kStatThreads) {
             Raw8<FP32> h;
             Raw8<false> g;
-            float w[8];
+            Raw8<WFP32> w;
             h.load(p.t, t * C + c);
             g.load(p.grad_y, t * C + c);
-            load_weight(p.weight, p.weight_fp32, c, w);
+            w.load_cached(p.weight, c);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 s0 = fmaf(h.get(e), h.get(e), s0);
-                s1 = fmaf(g.get(e) * w[e], h.get(e), s1);
+                s1 = fmaf(g.get(e) * w.get(e), h.get(e), s1);
             }
         }
         s0 = wave_sum(s0);
@@ -411,81 +412,88 @@ __global__ __launch_bounds__(kJoinWaves *kWave) void rms_norm_join_kernel(const 
 }
 
 constexpr int32_t kNormWide = 16384;  // wider rows' gradients take their statistics first
-constexpr int32_t kNormGradBlocks = 1024;
 
-int32_t grad_rows_per_block(int32_t H) { return H <= 2048 ? 4 : 1; }
+// Blocks of the gradient's kernel: about as many as the GPU holds at once, each
+// with a partial sum of the weight's gradient. Four rows a block up to 2048
+// columns, else one. (4099 x 7168 in float32: 82.6 us with 512, 85.4 with 1024.)
 int32_t grad_blocks(int64_t T, int32_t H)
 {
-    const int32_t rows = grad_rows_per_block(H);
-    const int64_t n = (T + rows - 1) / rows;
-    return (int32_t)(n < kNormGradBlocks ? n : kNormGradBlocks);
+    const int64_t n = H <= 2048 ? (T + 3) / 4 : T, most = H <= 4096 ? 1024 : 512;
+    return (int32_t)(n < most ? n : most);
 }
 
-template <bool FP32, int WPR, int CH>
+template <bool FP32, bool WFP32, int WPR, int CH>
 hipError_t launch_norm(const NormArgs &p, hipStream_t stream)
 {
     constexpr int kRows = norm_threads(WPR) / kWave / WPR;
     const int64_t blocks = (p.T + kRows - 1) / kRows;
-    hipLaunchKernelGGL((rms_norm_kernel<FP32, WPR, CH>), dim3((unsigned)(blocks < kMaxRowBlocks ? blocks : kMaxRowBlocks)),
-                       dim3(norm_threads(WPR)), 0, stream, p);
+    hipLaunchKernelGGL((rms_norm_kernel<FP32, WFP32, WPR, CH>),
+                       dim3((unsigned)(blocks < kMaxRowBlocks ? blocks : kMaxRowBlocks)), dim3(norm_threads(WPR)), 0,
+                       stream, p);
     return hipGetLastError();
 }
 
-template <bool FP32>
+// One wave per row and no barrier up to 2048 columns; wider rows take a wave
+// per 512 columns, which shortens a single row's way: 128 x 7168 took 4.4 us with
+// 16 waves and 5.8 with four.
+template <bool FP32, bool WFP32>
 hipError_t norm_by_width(const NormArgs &p, hipStream_t stream)
 {
     if (p.H <= 512)
-        return launch_norm<FP32, 1, 1>(p, stream);
+        return launch_norm<FP32, WFP32, 1, 1>(p, stream);
     if (p.H <= 1024)
-        return launch_norm<FP32, 1, 2>(p, stream);
+        return launch_norm<FP32, WFP32, 1, 2>(p, stream);
     if (p.H <= 2048)
-        return launch_norm<FP32, 1, 4>(p, stream);
+        return launch_norm<FP32, WFP32, 1, 4>(p, stream);
     if (p.H <= 4096)
-        return launch_norm<FP32, 4, 2>(p, stream);
+        return launch_norm<FP32, WFP32, 8, 1>(p, stream);
     if (p.H <= 8192)
-        return launch_norm<FP32, 4, 4>(p, stream);
+        return launch_norm<FP32, WFP32, 16, 1>(p, stream);
     if (p.H <= 16384)
-        return launch_norm<FP32, 8, 4>(p, stream);
+        return launch_norm<FP32, WFP32, 16, 2>(p, stream);
     if (p.H <= 32768)
-        return launch_norm<FP32, 16, 4>(p, stream);
-    return launch_norm<FP32, 16, 8>(p, stream);
+        return launch_norm<FP32, WFP32, 16, 4>(p, stream);
+    return launch_norm<FP32, WFP32, 16, 8>(p, stream);
 }
 
-template <bool FP32, int WPR, int CH, bool GIVEN = false>
+template <bool FP32, bool WFP32, int WPR, int CH, bool GIVEN = false>
 hipError_t launch_norm_grad(const NormGradArgs &p, int32_t blocks, hipStream_t stream)
 {
     const dim3 grid((unsigned)blocks, GIVEN ? (unsigned)((p.H + WPR * CH * 512 - 1) / (WPR * CH * 512)) : 1);
-    hipLaunchKernelGGL((rms_norm_backward_kernel<FP32, WPR, CH, GIVEN>), grid, dim3(norm_threads(WPR)), 0, stream, p);
+    hipLaunchKernelGGL((rms_norm_backward_kernel<FP32, WFP32, WPR, CH, GIVEN>), grid, dim3(norm_threads(WPR)), 0, stream,
+                       p);
     return hipGetLastError();
 }
 
-template <bool FP32>
+template <bool FP32, bool WFP32>
 hipError_t norm_grad_by_width(const NormGradArgs &p, hipStream_t stream)
 {
     const int32_t blocks = grad_blocks(p.T, p.H);
     if (p.H <= 512)
-        return launch_norm_grad<FP32, 1, 1>(p, blocks, stream);
+        return launch_norm_grad<FP32, WFP32, 1, 1>(p, blocks, stream);
     if (p.H <= 1024)
-        return launch_norm_grad<FP32, 1, 2>(p, blocks, stream);
+        return launch_norm_grad<FP32, WFP32, 1, 2>(p, blocks, stream);
     if (p.H <= 2048)
-        return launch_norm_grad<FP32, 1, 4>(p, blocks, stream);
+        return launch_norm_grad<FP32, WFP32, 1, 4>(p, blocks, stream);
     if (p.H <= 4096)
-        return launch_norm_grad<FP32, 4, 2>(p, blocks, stream);
+        return launch_norm_grad<FP32, WFP32, 8, 1>(p, blocks, stream);
     if (p.H <= 8192)
-        return launch_norm_grad<FP32, 4, 4>(p, blocks, stream);
+        return launch_norm_grad<FP32, WFP32, 8, 2>(p, blocks, stream);
     if (p.H <= kNormWide)
-        return launch_norm_grad<FP32, 8, 4>(p, blocks, stream);
-    hipLaunchKernelGGL(rms_norm_stats_kernel<FP32>, dim3((unsigned)(p.T < kMaxRowBlocks ? p.T : kMaxRowBlocks)),
+        return launch_norm_grad<FP32, WFP32, 16, 2>(p, blocks, stream);
+    hipLaunchKernelGGL((rms_norm_stats_kernel<FP32, WFP32>), dim3((unsigned)(p.T < kMaxRowBlocks ? p.T : kMaxRowBlocks)),
                        dim3(kStatThreads), 0, stream, p);
     const hipError_t err = hipGetLastError();
-    return err == hipSuccess ? launch_norm_grad<FP32, 4, 4, true>(p, blocks, stream) : err;
+    return err == hipSuccess ? launch_norm_grad<FP32, WFP32, 8, 2, true>(p, blocks, stream) : err;
 }
 
 }  // namespace
 
 hipError_t launch_rms_norm(const NormArgs &p, bool fp32, hipStream_t stream)
 {
-    return fp32 ? norm_by_width<true>(p, stream) : norm_by_width<false>(p, stream);
+    if (p.weight_fp32)
+        return fp32 ? norm_by_width<true, true>(p, stream) : norm_by_width<false, true>(p, stream);
+    return fp32 ? norm_by_width<true, false>(p, stream) : norm_by_width<false, false>(p, stream);
 }
 
 // partial sums of the weight's gradient, then the statistics of wide rows
@@ -501,7 +509,9 @@ hipError_t launch_rms_norm_backward(NormGradArgs p, bool fp32, bool accumulate, 
     p.partial = grad_weight ? static_cast<float *>(workspace) : nullptr;
     p.stats = static_cast<float *>(workspace) + (size_t)blocks * p.H;
     if (p.T > 0) {
-        const hipError_t err = fp32 ? norm_grad_by_width<true>(p, stream) : norm_grad_by_width<false>(p, stream);
+        const hipError_t err =
+            p.weight_fp32 ? (fp32 ? norm_grad_by_width<true, true>(p, stream) : norm_grad_by_width<false, true>(p, stream))
+                          : (fp32 ? norm_grad_by_width<true, false>(p, stream) : norm_grad_by_width<false, false>(p, stream));
         if (err != hipSuccess || !grad_weight)
             return err;
     }
