@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG, "libmoe_ep.so")
 
 SOURCES = ["api.hip", "route_topk.hip", "layout.hip", "permute.hip", "combine.hip", "regroup.hip", "fp8.hip", "expert.hip", "floor.hip", "route_layout.hip",
            "score_route.hip", "combine_backward.hip", "product.hip", "product_few.hip", "product_wgrad.hip",
-           "norm.hip", "quantize_weights.hip", "product_fp8.hip", "product_fp8_few.hip"]
+           "norm.hip", "quantize_weights.hip", "product_fp8.hip", "product_fp8_few.hip", "product_fp8_some.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",

@@ -198,7 +198,9 @@ struct Product8Args {
     int64_t a_bytes, out8_bytes;  // bytes of a row
 };
 hipError_t launch_product_fp8(const Product8Args &p, int32_t act, bool gated, bool grad, hipStream_t stream);
-hipError_t launch_product_fp8_few(const Product8Args &p, int32_t act, bool gated, hipStream_t stream);
+hipError_t launch_product_fp8_some(const Product8Args &p, int32_t act, bool gated, bool grad, int cus,
+                                   hipStream_t stream);
+hipError_t launch_product_fp8_few(const Product8Args &p, int32_t act, bool gated, int cus, hipStream_t stream);
 
 // Synthetic floor: a contiguous streaming read and write (floor.hip).
 hipError_t launch_hbm_floor(const void *src, int64_t read_bytes, void *dst, int64_t write_bytes,

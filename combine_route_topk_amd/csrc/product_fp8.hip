@@ -10,7 +10,7 @@
 // scale is the same for a wave's columns across a K-tile: the MFMA starts from
 // zero and its sum is added to the accumulators times the scale, four FMAs of
 // 4 cycles beside an MFMA of 32.
-#include "product_tile.hpp"
+#include "product_fp8_device.hpp"
 
 namespace moe {
 namespace {
@@ -22,32 +22,6 @@ constexpr int kStage8 = 2 * kHalfBytes, kB8 = 2 * kStage8, kScales8 = 2 * kB8;
 constexpr int kScaleStage = kTile * 16;
 constexpr uint32_t kBehind = 0x40000000u;  // past the end of every operand of a tile, and no carry with `from`
 constexpr int kLds8 = kScales8 + 2 * kScaleStage;
-// A load of 16 bytes per lane into LDS, at `dst` and 16 bytes on for each lane.
-// It is written as an instruction (it has no register result) so that the
-// compiler does not know of it: it would wait for all such loads in flight
-// before every LDS read. The schedule below orders them with barriers and
-// counted waits instead. (M0 cannot be named as overwritten; nothing else in
-// these kernels uses it.)
-__device__ __forceinline__ void load_to_lds(uint32_t dst, u32x4 r, uint32_t off, uint32_t soff)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :
-                 : "s"(dst), "v"(off), "s"(r), "s"(soff)
-                 : "memory");
-}
-
-__device__ __forceinline__ u32x4 descriptor(const uint8_t *p, uint32_t records)
-{
-    const uint64_t at = (uint64_t)(uintptr_t)p;
-    return u32x4{(uint32_t)at, (uint32_t)(at >> 32), records, (uint32_t)kGemmBufferFlags};
-}
-
-template <class T>
-__device__ __forceinline__ T lds_read(uint32_t at)
-{
-    return *(__attribute__((address_space(3))) const T *)(uintptr_t)at;
-}
-
 // Fragments of A (four of 16 rows) and B (two of 16 columns): 128 k of a row in
 // four lanes, a lane's 32 in two pieces of 16 that lie 64 apart.
 struct FragA8 {
@@ -57,12 +31,6 @@ struct FragA8 {
 struct FragB8 {
     i32x8 v[2];
 };
-__device__ __forceinline__ i32x8 read_frag(uint32_t at0, uint32_t at1)
-{
-    const i32x4 lo = lds_read<i32x4>(at0), hi = lds_read<i32x4>(at1);
-    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
 // A block's scale s of the weights as the product of the power of two that the
 // MFMA multiplies by, and of a factor of magnitude [1, 2). Accumulators are kept
 // in units of the factor: they are multiplied by the old one over the new where
@@ -429,22 +397,9 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_fp8_kernel(Product8Ar
     }
 }
 
-// Whether the kernel for few rows is the faster one, as for bf16.
-bool few_rows(int64_t max_rows, int32_t El, int32_t K, int64_t col_tiles)
-{
-    const int64_t tiles = (max_rows < El ? max_rows : El) * col_tiles;
-    if (tiles < 256)
-        return max_rows <= 20 * (int64_t)El;
-    return K < 4096 && max_rows <= 16 * (int64_t)El;
-}
-
 template <bool GRAD>
-hipError_t launch(const Product8Args &p, int32_t act, bool gated, hipStream_t stream)
+hipError_t launch(const Product8Args &p, int32_t act, bool gated, int cus, hipStream_t stream)
 {
-    int cus = 0;
-    const hipError_t err = current_cus(&cus);
-    if (err != hipSuccess)
-        return err;
     const int kCols = gated && !GRAD ? kTile / 2 : kTile;
     // four blocks a tile, for its slices
     const int64_t units = 4 * ((int64_t)p.max_rows / kTile + p.El) * ((p.N + kCols - 1) / kCols);
@@ -468,13 +423,51 @@ hipError_t launch(const Product8Args &p, int32_t act, bool gated, hipStream_t st
 #undef MOE_PRODUCT_CASE
 }
 
+// Which kernel a product runs on. The host knows max_rows, not how the rows lie:
+// it takes hit = min(max_rows, E_l) experts with rows, and a half-full tile for
+// each beside the full ones. On MI355X, in us, few rows / some rows / tiles:
+//   tiles of 64 rows for less than a quarter of the CUs: 1 expert, 7168 by 2 x
+//   2048: 18 / 42 / 90 at 1 row, 27 / 52 / 91 at 128; 8 experts, 2048 by 2 x 768:
+//   18 / 20 / 32 at 64 rows each;
+//   for less than all: 4 experts, 7168 by 7168: 38 / 47 / 90 at 4 rows each,
+//   49 / 43 / 93 at 16, 113 / 55 / 91 at 64;
+//   for all: 32 experts, 7168 by 2 x 2048: 166 / 161 / 206 at one row each,
+//   216 / 164 / 189 at 32, 370 / 169 / 193 at 64, 715 / 249 / 220 at 128; 64
+//   experts, 2048 by 2048: 42 / 43 / 62 at one, 169 / 59 / 65 at 64.
+// A round of tiles over the CUs takes about 1.1 us for each 128 k with 64 rows
+// and 1.9 with 256, which decides between these two.
+enum class Kernel { kFew, kSome, kTiles };
+Kernel choose(const Product8Args &p, bool gated, bool grad, int cus)
+{
+    const int64_t rows = p.max_rows, hit = rows < p.El ? rows : p.El;
+    const int64_t columns = gated && !grad ? kTile / 2 : kTile, across = (p.N + columns - 1) / columns;
+    auto tiles = [&](int64_t height) {
+        const int64_t n = rows / height + hit / 2;
+        return (n > hit ? n : hit) * across;
+    };
+    auto rounds = [&](int64_t n) { return (n + cus - 1) / cus; };
+    const int64_t t64 = tiles(64);
+    if (!grad && (4 * t64 < cus ? rows <= 128 * (int64_t)p.El : t64 < cus && rows <= 8 * (int64_t)p.El))
+        return Kernel::kFew;
+    return rounds(t64) * 11 <= rounds(tiles(kTile)) * 19 ? Kernel::kSome : Kernel::kTiles;
+}
+
 }  // namespace
 
 hipError_t launch_product_fp8(const Product8Args &p, int32_t act, bool gated, bool grad, hipStream_t stream)
 {
-    if (!grad && few_rows(p.max_rows, p.El, p.K, (p.N + (gated ? kTile / 2 : kTile) - 1) / (gated ? kTile / 2 : kTile)))
-        return launch_product_fp8_few(p, act, gated, stream);
-    return grad ? launch<true>(p, act, gated, stream) : launch<false>(p, act, gated, stream);
+    int cus = 0;
+    const hipError_t err = current_cus(&cus);
+    if (err != hipSuccess)
+        return err;
+    switch (choose(p, gated, grad, cus)) {
+    case Kernel::kFew:
+        return launch_product_fp8_few(p, act, gated, cus, stream);
+    case Kernel::kSome:
+        return launch_product_fp8_some(p, act, gated, grad, cus, stream);
+    default:
+        return grad ? launch<true>(p, act, gated, cus, stream) : launch<false>(p, act, gated, cus, stream);
+    }
 }
 
 }  // namespace moe

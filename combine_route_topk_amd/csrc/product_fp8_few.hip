@@ -8,7 +8,7 @@
 // row, and add their sums through LDS, in the waves' order. A lane's two
 // 16-byte pieces of 128 values lie 64 bytes apart: that is where the scaled
 // MFMA's lanes hold them, and its scales, one per 32 values, follow from it.
-#include "product_tile.hpp"
+#include "product_fp8_device.hpp"
 
 namespace moe {
 namespace {
@@ -65,51 +65,6 @@ __device__ __forceinline__ void few_step(const FewOperands<MT, NG> &o, uint32_t 
             for (int e = 0; e < 4; ++e)
                 c[g][m][e] = fmaf(w[g >> 1], p[e], c[g][m][e]);
         }
-}
-
-// 32 columns from n0 of 16 rows, a row in lanes i, i + 16, i + 32 and i + 48:
-// columns j * 16 + (lane / 16) * 4 + 0..3 of sums z[j] (gated: and those that
-// they gate, u[j]). Bias, activation, gate and residual, then the one rounding
-// of each output. Lanes with `in` false take part in the row's maximum only.
-template <bool GATED, int ACT>
-__device__ __forceinline__ void finish32(const Product8Args &p, int32_t l, int64_t row, bool in, int32_t n0, int lane,
-                                         f32x4 (&z)[2], f32x4 (&u)[2])
-{
-    const int64_t wide = GATED ? 2 * (int64_t)p.N : p.N;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int32_t c = n0 + j * 16 + (lane >> 4) * 4;
-        auto read = [](const uint16_t *q) { return widen(*reinterpret_cast<const u32x2 *>(q)); };
-        auto write = [](uint16_t *q, f32x4 v) { *reinterpret_cast<u32x2 *>(q) = narrow(v); };
-        if (p.bias) {
-            z[j] += read(p.bias + l * wide + c);
-            if (GATED)
-                u[j] += read(p.bias + l * wide + p.N + c);
-        }
-        if (p.pre_out && in) {
-            write(p.pre_out + row * wide + c, z[j]);
-            if (GATED)
-                write(p.pre_out + row * wide + p.N + c, u[j]);
-        }
-        f32x4 r = {0.f, 0.f, 0.f, 0.f};
-        if (p.residual && in)
-            r = read(p.residual + row * p.N + c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            z[j][e] = (GATED ? act<ACT>(z[j][e]) * u[j][e] : act<ACT>(z[j][e])) + r[e];
-        if (p.out && in)
-            write(p.out + row * p.N + c, z[j]);
-    }
-    if (p.out8) {
-        uint32_t codes[2];
-        const uint32_t scale = encode32(z, codes);
-        uint8_t *at = p.out8 + row * p.out8_bytes;
-        if (in) {
-            *reinterpret_cast<u32x2 *>(at + n0 + (lane >> 4) * 8) = u32x2{codes[0], codes[1]};
-            if (lane < 16)
-                at[p.N + n0 / 32] = (uint8_t)scale;
-        }
-    }
 }
 
 template <int MT, int NG, bool GATED, int ACT>
@@ -201,12 +156,8 @@ __global__ __launch_bounds__(kFewThreads, 4) void product_fp8_few_kernel(Product
 
 }  // namespace
 
-hipError_t launch_product_fp8_few(const Product8Args &p, int32_t act, bool gated, hipStream_t stream)
+hipError_t launch_product_fp8_few(const Product8Args &p, int32_t act, bool gated, int cus, hipStream_t stream)
 {
-    int cus = 0;
-    const hipError_t err = current_cus(&cus);
-    if (err != hipSuccess)
-        return err;
     const int64_t tiles = ((int64_t)p.max_rows / kFewRows + p.El) * (p.N / kFewCols);
     const dim3 grid((unsigned)(tiles < 2 * cus ? tiles : 2 * cus));
 #define MOE_FEW_CASE(A)                                                                                        \

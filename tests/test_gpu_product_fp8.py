@@ -160,10 +160,43 @@ def test_dgrad_in_place_and_wide(moe):
     run_dgrad(moe, [9, 260], 8224, 96)
 
 
+# Rows and columns enough for tiles of 256 rows, which few of the sizes above are: rows of 64 for over 256 blocks.
+MANY = [[4200], [1300, 0, 2900, 1], [257] * 16, [255, 1, 64, 0, 192, 3690], [31, 4000, 65, 129]]
+
+
+@pytest.mark.parametrize("counts", MANY)
+@pytest.mark.parametrize("H", [32, 96, 128, 224, 256, 544, 1056])
+def test_product_many_rows(moe, counts, H):
+    run_product(moe, counts, H, 1184, pad=2)
+    run_product(moe, counts, H, 640, "silu", True, pre=True, pad=1)
+
+
+@pytest.mark.parametrize("kind", ref.ACTS)
+def test_product_many_rows_epilogues(moe, kind):
+    for gated, O in ((False, 1184), (True, 608)):
+        for bias, residual, pre, out in ((True, True, True, "both"), (False, True, False, "bf16"), (False, False, True, "fp8")):
+            run_product(moe, MANY[1], 192, O, kind, gated, bias, residual, pre, out, pad=3)
+    run_product(moe, MANY[3], 128, 1312, kind, False, True, True, True, pad=4, in_place=True)
+
+
+@pytest.mark.parametrize("counts", MANY)
+@pytest.mark.parametrize("O", [32, 160, 384, 1056])
+def test_dgrad_many_rows(moe, counts, O):
+    run_dgrad(moe, counts, O, 1184, pad=2)
+    run_dgrad(moe, counts, O, 1184, "silu", True, True, pad=1)
+
+
+@pytest.mark.parametrize("kind", ref.ACTS)
+def test_dgrad_many_rows_activations(moe, kind):
+    for gated, out in ((False, "both"), (True, "fp8"), (True, "bf16"), (False, "fp8")):
+        run_dgrad(moe, MANY[1], 192, 1184, kind, gated, True, out, pad=3)
+    run_dgrad(moe, MANY[3], 128, 1312, kind, True, True, "both", 2, in_place=True)
+
+
 def test_offsets_out_of_range(moe):
     """Offsets past the buffer are clamped, and where they decrease nothing is computed."""
     rng = np.random.default_rng(5)
-    for rows, O in ((40, 64), (600, 512)):
+    for rows, O in ((40, 64), (600, 512), (4200, 1184)):
         x, xv = rows8(rng, rows, 128)
         W, s, Wv = weights8(rng, 3, O, 128)
         for off, used in (([-5, 10, 20, rows + 1000], rows), ([0, 30, 20, 25], 0)):
@@ -178,12 +211,12 @@ def test_offsets_out_of_range(moe):
             f8.assert_rows8(y8, wy, ey, used, "y8")
 
 
-@pytest.mark.parametrize("counts", [[3, 4], [300, 20]])
-def test_nan_and_infinities(moe, counts):
+@pytest.mark.parametrize("counts,O", [([3, 4], 96), ([300, 20], 96), ([4000, 300], 1184)])
+def test_nan_and_infinities(moe, counts, O):
     """A NaN code or scale reaches its own row's results, or its own column's, and no others; codes and scales past K,
     in the padding, and of other rows do not. An infinite result becomes a NaN code, and bf16's infinity."""
     rng = np.random.default_rng(6)
-    H, O = 160, 96  # K ends inside a step of 128, scale bytes inside a word
+    H = 160  # K ends inside a step of 128, scale bytes inside a word
     off = offsets(counts)
     n = int(off[-1])
     say("NaN", counts)
@@ -209,27 +242,32 @@ def test_nan_and_infinities(moe, counts):
     assert (np.isnan(d) == (bad | inf)).all()
 
 
-def test_weights_past_32_bits(moe):
-    """Weights past 2^31 bytes: the last expert's rows against the same product on its weights alone."""
+@pytest.mark.parametrize("rows", [2, 300, 9000])
+def test_weights_past_32_bits(moe, rows):
+    """Weights past 2^31 bytes, on each kernel: the last expert's rows, against float64 (9000 rows: against the same
+    product on its weights alone, which the same kernel computes in the same order)."""
     El, O, H = 40, 2048, 7168
-    say("large", El, O, H)
+    say("large", El, O, H, rows)
     g = torch.Generator(device=DEV).manual_seed(0)
     W = torch.randint(0, 0x70, (El, 2 * O, H), generator=g, device=DEV, dtype=torch.uint8)
     s = torch.rand(El, 2 * O // 128, H // 128, generator=g, device=DEV) * 1e-3
-    for rows in (2, 300):
-        x = gpu(rows8(np.random.default_rng(1), rows, H)[0])
-        off = torch.zeros(El + 1, dtype=torch.int32, device=DEV)
-        off[El] = rows
-        big = moe.moe_expert_product_fp8(x, off, W, s, act="silu", gated=True, fp8=True)
-        one = moe.moe_expert_product_fp8(x, off[El - 1:].contiguous(), W[El - 1:].contiguous(), s[El - 1:].contiguous(),
-                                         act="silu", gated=True, fp8=True)
+    x, xv = rows8(np.random.default_rng(1), rows, H)
+    off = torch.zeros(El + 1, dtype=torch.int32, device=DEV)
+    off[El] = rows
+    y, y8 = moe.moe_expert_product_fp8(gpu(x), off, W, s, act="silu", gated=True, fp8=True)
+    W, s = W[El - 1:].contiguous(), s[El - 1:].contiguous()
+    if rows == 9000:
+        z, z8 = moe.moe_expert_product_fp8(gpu(x), off[El - 1:].contiguous(), W, s, act="silu", gated=True, fp8=True)
         torch.cuda.synchronize()
-        assert all(bool(torch.isfinite(t.float()).all()) for t in (big[0], one[0])) and bool((one[0] != 0).any())
-        if rows > 20:  # the same kernel: the same bits
-            assert torch.equal(big[0], one[0]) and torch.equal(big[1], one[1])
-        else:
-            a, b = big[0].float(), one[0].float()
-            assert float(((a - b).abs() / b.abs().clamp(min=1e-3)).max()) < 0.05
+        assert bool(torch.isfinite(y.float()).all()) and bool((y != 0).any())
+        assert torch.equal(y, z) and torch.equal(y8, z8)
+        return
+    torch.cuda.synchronize()
+    W, s = W.cpu().numpy(), s.cpu().numpy()
+    wy, _, _, ey = f8.product(xv, f8.rows_largest(x, H), np.array([0, rows]), f8.decode_weights(W, s), f8.weights_largest(W, s),
+                              kind="silu", gated=True)
+    assert_rows(y, wy, ey, rows, "y")
+    f8.assert_rows8(y8, wy, ey, rows, "y8")
 
 
 def test_rows_past_32_bits(moe):
@@ -244,14 +282,14 @@ def test_rows_past_32_bits(moe):
     s = torch.full((1, O // 128, H // 128), 1e-3, device=DEV)
     off = torch.tensor([0, n], dtype=torch.int32, device=DEV)
     y, y8 = moe.moe_expert_product_fp8(x, off, W, s, fp8=True)
-    k = 512
+    k = 9000  # enough for the same kernel
     z, z8 = moe.moe_expert_product_fp8(x[n - k:].contiguous(), torch.tensor([0, k], dtype=torch.int32, device=DEV), W, s,
                                        fp8=True)
     torch.cuda.synchronize()
     assert torch.equal(y[n - k:], z) and torch.equal(y8[n - k:], z8)
 
 
-@pytest.mark.parametrize("counts,H,O", [([3, 0, 2, 9], 512, 256), ([200, 0, 313, 41], 1024, 512)])
+@pytest.mark.parametrize("counts,H,O", [([3, 0, 2, 9], 512, 256), ([200, 0, 313, 41], 1024, 512), ([2000, 0, 2300, 41], 1184, 640)])
 def test_captured_and_replayed(moe, counts, H, O):
     """A layer's two products captured on a stream of their own, replayed on new rows and new offsets."""
     rng = np.random.default_rng(2)
