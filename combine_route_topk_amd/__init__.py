@@ -722,7 +722,9 @@ _U8 = (torch.uint8,)
 
 
 def _row8(H: int) -> int:
-    """moe_fp8_row_bytes of a width that the call itself checks, without a call."""
+    """moe_fp8_row_bytes of a width whose limits the call that follows checks, without a call of its own."""
+    if H % 32:
+        raise MoeError("moe_fp8_row_bytes", MOE_ERR_UNSUPPORTED)
     return H + 128 * ((H + 4095) // 4096)
 
 
