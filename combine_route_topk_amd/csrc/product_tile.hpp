@@ -14,12 +14,6 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kOne = 127;  // the scale byte of 1
 
-__device__ __forceinline__ i32x8 join8(bf16x8 lo, bf16x8 hi)
-{
-    const i32x4 a = __builtin_bit_cast(i32x4, lo), b = __builtin_bit_cast(i32x4, hi);
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
 // a scalar load: `p` is the same in every lane and not written by this kernel
 typedef __attribute__((address_space(4))) const float *uniform_floats;
 __device__ __forceinline__ float load_uniform(const float *p) { return *(uniform_floats)(uintptr_t)p; }
