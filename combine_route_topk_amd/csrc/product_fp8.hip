@@ -415,6 +415,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_fp8_kernel(Product8Ar
         wait_loads<0>();
         slot_end();
     }
+    static_assert(kSomeThreads == kGemmThreads && kSomeRows * 4 == kTile && kSomeCols == kTile);
     // A round of slices of 64 rows: product_fp8_some.hpp's loads run further
     // ahead, 1.1 us for each 128 k where the loop above takes 1.65.
     if (slices == 4 && u < units) {

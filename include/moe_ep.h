@@ -772,8 +772,9 @@ moe_status_t moe_expert_product_wgrad(const uint16_t *grad_y, const uint16_t *x,
  * are each one rounding of v. y is what the router reads, and y8 has the
  * format of moe_dispatch_permute_fp8's rows (codes, scale bytes, zero padding):
  * moe_dispatch_permute moves FP8 rows as bf16 rows of moe_fp8_row_bytes(H) / 2
- * columns, and moe_expert_product_fp8 multiplies them. A value that is NaN or
- * infinite becomes a NaN code; a row that holds one is NaN throughout.
+ * columns, and moe_expert_product_fp8 multiplies them. A v that is NaN
+ * becomes a NaN code. A row of total with a NaN gives NaN throughout, one with
+ * an infinity NaN there and zeros elsewhere.
  *
  * Defined by: ai-from-scratch "19. All-to-all", intro (every token's vector
  * after attention enters the layer) and "MoE All-to-All Dispatch and Ragged

@@ -242,6 +242,40 @@ def test_nan_and_infinities(moe, counts, O):
     assert (np.isnan(d) == (bad | inf)).all()
 
 
+@pytest.mark.parametrize("counts,O", [([3, 4], 96), ([300, 20], 96), ([4000, 300], 1184)])
+def test_scales_of_every_size(moe, counts, O):
+    """Negative, huge, least normal, subnormal and zero scales of the weights on each kernel; NaN and infinite ones reach
+    the columns of their block, in their expert's rows, and nothing else."""
+    rng = np.random.default_rng(7)
+    H = 384
+    off = offsets(counts)
+    n = int(off[-1])
+    say("scales", counts, O)
+    x, xv = rows8(rng, n, H)
+    W, s, _ = weights8(rng, 2, O, H)
+    s[0, 0] = [-0.75, 2.0 ** -140, 1.5 * 2.0 ** 90]
+    s[1, 0] = [0.0, 2.0 ** -126, -1.25 * 2.0 ** -100]
+    for bad in (False, True):
+        if bad:
+            s[0, 0, 1], s[1, 0, 2] = np.nan, np.inf
+        y, y8 = canary(n, O), empty8(n, O)
+        moe.moe_expert_product_fp8(gpu(x), gpu(off), gpu(W), gpu(s), y=y, y8=y8)
+        torch.cuda.synchronize()
+        if bad:
+            got, d = dn(y.cpu()), f8.decode_rows(y8.cpu().numpy(), O)
+            assert not np.isfinite(got[:, :128]).any() and np.isnan(d[:, :128]).all()
+            assert np.isfinite(got[:, 128:]).all() and np.isfinite(d[:, 128:]).all()
+            continue
+        wy, _, _, ey = f8.product(xv, f8.rows_largest(x, H), off, f8.decode_weights(W, s), f8.weights_largest(W, np.abs(s)))
+        # a scale below 2^-126 may count as 2^-127
+        codes = np.abs(f8.e4m3(W)).max(2)
+        for l in range(2):
+            b, e = off[l], off[l + 1]
+            ey[b:e] += 2.0 ** -126 * np.abs(xv[b:e]).sum(1)[:, None] * codes[l]
+        assert_rows(y, wy, ey, n, "y")
+        f8.assert_rows8(y8, wy, ey, n, "y8")
+
+
 @pytest.mark.parametrize("rows", [2, 300, 9000])
 def test_weights_past_32_bits(moe, rows):
     """Weights past 2^31 bytes, on each kernel: the last expert's rows, against float64 (9000 rows: against the same
