@@ -29,44 +29,80 @@ __device__ __forceinline__ float wave_sum(float v)
     return __uint_as_float(readlane_u32(__float_as_uint(v), kWave - 1));
 }
 
-// Eight consecutive values as they lie in memory, bf16 or float32.
-template <bool FP32>
+// A lane's eight columns of 512 that a wave takes: neighbours, or (SPLIT) two
+// fours 256 apart, so that float32 rows too are read and written as consecutive
+// bytes of a wave (8192 x 7168: forward 135 against 154 us, gradient 141 against
+// 154).
+template <bool SPLIT>
+struct Columns {
+    static constexpr int kParts = SPLIT ? 2 : 1;
+    int32_t first;  // the same in every lane
+    uint32_t mine;  // the lane's first, from there
+    __device__ __forceinline__ Columns(int32_t first_, int lane) : first(first_), mine(lane * (SPLIT ? 4 : 8)) {}
+    __device__ __forceinline__ int32_t start(int k) const { return first + k * 256; }
+    __device__ __forceinline__ int32_t at(int k) const { return start(k) + (int32_t)mine; }
+    __device__ __forceinline__ bool in(int k, int32_t H) const { return (int32_t)mine < H - start(k); }
+};
+
+// Their values as they lie in memory, bf16 or float32; zeros where there is no
+// column or row.
+template <bool FP32, bool SPLIT>
 struct Raw8 {
-    u32x4 q[FP32 ? 2 : 1];
-    // rows, each once: past the caches (105 against 113 us, 32768 x 2048 forward)
-    __device__ __forceinline__ void load(const void *p, int64_t chunk)
+    static constexpr int kWords = FP32 ? 8 : 4, kPart = kWords / Columns<SPLIT>::kParts;
+    typedef uint32_t piece __attribute__((ext_vector_type(kPart < 4 ? kPart : 4)));  // of one load
+    static constexpr int kPiece = kPart < 4 ? kPart : 4;
+    static constexpr int kSize = FP32 ? 4 : 2;
+    uint32_t q[kWords];
+    __device__ __forceinline__ void clear()
     {
-        const u32x4 *s = static_cast<const u32x4 *>(p) + chunk * (FP32 ? 2 : 1);
-        q[0] = load_stream(s);
-        if (FP32)
-            q[FP32 ? 1 : 0] = load_stream(s + 1);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            q[i] = 0;
     }
-    __device__ __forceinline__ void store(void *p, int64_t chunk) const
+    // part k of columns c of the row that begins at element `row`, the same in every lane
+    template <bool STREAM>
+    __device__ __forceinline__ void load_as(const void *p, int64_t row, const Columns<SPLIT> &c, int k)
     {
-        u32x4 *s = static_cast<u32x4 *>(p) + chunk * (FP32 ? 2 : 1);
-        store_stream(s, q[0]);
-        if (FP32)
-            store_stream(s + 1, q[FP32 ? 1 : 0]);
+        const piece *s = reinterpret_cast<const piece *>(static_cast<const uint8_t *>(p) + (row + c.start(k)) * kSize +
+                                                         c.mine * (uint32_t)kSize);
+#pragma unroll
+        for (int u = 0; u < kPart / kPiece; ++u) {
+            const piece v = STREAM ? __builtin_nontemporal_load(s + u) : s[u];
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i)
+                q[k * kPart + u * kPiece + i] = v[i];
+        }
+    }
+    // rows, each once: past the caches (105 against 113 us, 32768 x 2048 forward)
+    __device__ __forceinline__ void load(const void *p, int64_t row, const Columns<SPLIT> &c, int k)
+    {
+        load_as<true>(p, row, c, k);
     }
     // the weight, for every row
-    __device__ __forceinline__ void load_cached(const void *p, int64_t chunk)
+    __device__ __forceinline__ void load_cached(const void *p, const Columns<SPLIT> &c, int k) { load_as<false>(p, 0, c, k); }
+    __device__ __forceinline__ void store(void *p, int64_t row, const Columns<SPLIT> &c, int k) const
     {
-        const u32x4 *s = static_cast<const u32x4 *>(p) + chunk * (FP32 ? 2 : 1);
-        q[0] = s[0];
-        if (FP32)
-            q[FP32 ? 1 : 0] = s[1];
+        piece *s = reinterpret_cast<piece *>(static_cast<uint8_t *>(p) + (row + c.start(k)) * kSize + c.mine * (uint32_t)kSize);
+#pragma unroll
+        for (int u = 0; u < kPart / kPiece; ++u) {
+            piece v;
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i)
+                v[i] = q[k * kPart + u * kPiece + i];
+            __builtin_nontemporal_store(v, s + u);
+        }
     }
     __device__ __forceinline__ float get(int i) const
     {
         if (FP32)
-            return __uint_as_float(q[FP32 ? i >> 2 : 0][i & 3]);
-        return i & 1 ? bf16_hi(q[0][i >> 1]) : bf16_lo(q[0][i >> 1]);
+            return __uint_as_float(q[i % kWords]);
+        return i & 1 ? bf16_hi(q[i >> 1]) : bf16_lo(q[i >> 1]);
     }
     __device__ __forceinline__ void set(const float (&v)[8])
     {
 #pragma unroll
-        for (int i = 0; i < (FP32 ? 8 : 4); ++i)
-            q[FP32 ? i >> 2 : 0][i & 3] = FP32 ? __float_as_uint(v[i]) : pack_bf16x2(v[2 * i & 7], v[(2 * i + 1) & 7]);
+        for (int i = 0; i < kWords; ++i)
+            q[i] = FP32 ? __float_as_uint(v[i]) : pack_bf16x2(v[2 * i & 7], v[(2 * i + 1) & 7]);
     }
 };
 
@@ -80,13 +116,15 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_kernel(NormArgs p)
 {
     constexpr int kRows = norm_threads(WPR) / kWave / WPR;
     constexpr int kLines = (WPR * CH * 512 + 4095) / 4096;
-    constexpr bool kEarly = CH <= 4;  // wider rows need the registers
+    // wider rows need the registers: the weight is read when it is used, the
+    // residual by a few chunks (float32, 1024 x 40960: 104 us, 213 with spills)
+    constexpr bool kEarly = WPR < 16 || CH <= 2;
+    constexpr int kBatch = kEarly ? CH : (FP32 ? 2 : 4);
     __shared__ float part[2][kRows][WPR];
     __shared__ __attribute__((aligned(16))) uint8_t scales[kRows][kLines * kScaleLine];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int slot = wave / WPR, wr = wave % WPR;  // the wave's row of the block, and its place in it
-    const int32_t C = p.H / 8;
     const int32_t pad = (p.H + 4095) / 4096 * kScaleLine;  // scale bytes of a row
     if (p.y8) {  // padding stays zero: no wave writes it below
         for (int i = threadIdx.x; i < kRows * kLines * kScaleLine / 4; i += norm_threads(WPR))
@@ -96,48 +134,57 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_kernel(NormArgs p)
     int parity = 0;
     for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += (int64_t)gridDim.x * kRows) {
         const int64_t t = t0 + slot;
-        const bool valid = t < p.T;
-        Raw8<FP32> h[CH];
-        Raw8<WFP32> w[CH];
+        const int32_t H = t < p.T ? p.H : 0;  // no columns in a row past the last
+        Raw8<FP32, FP32> h[CH];
+        Raw8<WFP32, FP32> w[CH];
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int32_t c = (i * WPR + wr) * kWave + lane;
-            if (valid && c < C) {
-                h[i].load(p.x, t * C + c);
-                if (kEarly)
-                    w[i].load_cached(p.weight, c);
-            }
+            const Columns<FP32> c((i * WPR + wr) * 512, lane);
+            h[i].clear();
+            w[i].clear();
+#pragma unroll
+            for (int k = 0; k < c.kParts; ++k)
+                if (c.in(k, H)) {
+                    h[i].load(p.x, t * p.H, c, k);
+                    if (kEarly)
+                        w[i].load_cached(p.weight, c, k);
+                }
         }
         if (p.residual) {
-            Raw8<FP32> r[CH];
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int32_t c = (i * WPR + wr) * kWave + lane;
-                if (valid && c < C)
-                    r[i].load(p.residual, t * C + c);
-            }
+            for (int first = 0; first < CH; first += kBatch) {
+                Raw8<FP32, FP32> r[kBatch];
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int32_t c = (i * WPR + wr) * kWave + lane;
-                if (valid && c < C) {
+                for (int b = 0; b < kBatch; ++b) {
+                    const Columns<FP32> c(((first + b) * WPR + wr) * 512, lane);
+                    r[b].clear();
+#pragma unroll
+                    for (int k = 0; k < c.kParts; ++k)
+                        if (c.in(k, H))
+                            r[b].load(p.residual, t * p.H, c, k);
+                }
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    const int i = first + b;
+                    const Columns<FP32> c((i * WPR + wr) * 512, lane);
                     float v[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        v[e] = h[i].get(e) + r[i].get(e);
+                        v[e] = h[i].get(e) + r[b].get(e);
                     h[i].set(v);
-                    h[i].store(p.total, t * C + c);
+#pragma unroll
+                    for (int k = 0; k < c.kParts; ++k)
+                        if (c.in(k, H))
+                            h[i].store(p.total, t * p.H, c, k);
                 }
             }
         }
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int32_t c = (i * WPR + wr) * kWave + lane;
-            if (valid && c < C)
+        for (int i = 0; i < CH; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    sum = fmaf(h[i].get(e), h[i].get(e), sum);
-        }
+            for (int e = 0; e < 8; ++e)
+                sum = fmaf(h[i].get(e), h[i].get(e), sum);
         sum = wave_sum(sum);
         if (WPR > 1) {
             if (lane == 0)
@@ -152,32 +199,51 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_kernel(NormArgs p)
         const float r = rsqrtf(sum / (float)p.H + p.eps);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int32_t c = (i * WPR + wr) * kWave + lane;
-            if (!valid || c >= C)
-                continue;
+            const Columns<FP32> c((i * WPR + wr) * 512, lane);
             if (!kEarly)
-                w[i].load_cached(p.weight, c);
-            float v[8], m = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+                for (int k = 0; k < c.kParts; ++k)
+                    if (c.in(k, H))
+                        w[i].load_cached(p.weight, c, k);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
                 v[e] = h[i].get(e) * r * w[i].get(e);
-                m = max_abs(m, v[e]);
-            }
-            if (p.y) {
-                Raw8<false> o;
-                o.set(v);
-                o.store(p.y, t * C + c);
-            }
-            if (p.y8) {
-                // H is a multiple of 32: the four lanes of a block are all here
-                m = fmaxf(m, __uint_as_float(dpp::mov<dpp::kQuadSwap1>(__float_as_uint(m), 0u)));
-                m = fmaxf(m, __uint_as_float(dpp::mov<dpp::kQuadSwap2>(__float_as_uint(m), 0u)));
-                const int32_t e = fp8_exponent(m);
-                const float mul = fp8_multiplier(e);
-                const u32x2 codes = {fp8_encode4(v[0], v[1], v[2], v[3], mul), fp8_encode4(v[4], v[5], v[6], v[7], mul)};
-                __builtin_nontemporal_store(codes, reinterpret_cast<u32x2 *>(p.y8 + t * p.y8_bytes) + c);
-                if ((lane & 3) == 0)
-                    scales[slot][c >> 2] = (uint8_t)(e + 127);
+            Raw8<false, FP32> o;
+            o.set(v);
+#pragma unroll
+            for (int k = 0; k < c.kParts; ++k) {
+                if (!c.in(k, H))
+                    continue;
+                if (p.y)
+                    o.store(p.y, t * p.H, c, k);
+                if (p.y8) {
+                    // H is a multiple of 32: the lanes of a block, four or eight, are all here
+                    constexpr int kValues = 8 / Columns<FP32>::kParts;
+                    float m = 0.f;
+#pragma unroll
+                    for (int e = 0; e < kValues; ++e)
+                        m = max_abs(m, v[k * kValues + e]);
+                    m = fmaxf(m, __uint_as_float(dpp::mov<dpp::kQuadSwap1>(__float_as_uint(m), 0u)));
+                    m = fmaxf(m, __uint_as_float(dpp::mov<dpp::kQuadSwap2>(__float_as_uint(m), 0u)));
+                    if (FP32)
+                        m = fmaxf(m, __uint_as_float(dpp::mov<dpp::kRowHalfMirror>(__float_as_uint(m), 0u)));
+                    const int32_t e = fp8_exponent(m);
+                    const float mul = fp8_multiplier(e);
+                    uint32_t codes[kValues / 4];
+#pragma unroll
+                    for (int u = 0; u < kValues / 4; ++u) {
+                        const int f = k * kValues + u * 4;
+                        codes[u] = fp8_encode4(v[f], v[f + 1], v[f + 2], v[f + 3], mul);
+                    }
+                    uint8_t *at = p.y8 + (t * p.y8_bytes + c.start(k)) + c.mine;
+                    if constexpr (kValues == 8)
+                        __builtin_nontemporal_store(u32x2{codes[0], codes[1]}, reinterpret_cast<u32x2 *>(at));
+                    else
+                        __builtin_nontemporal_store(codes[0], reinterpret_cast<uint32_t *>(at));
+                    if ((lane & (32 / kValues - 1)) == 0)
+                        scales[slot][c.at(k) >> 5] = (uint8_t)(e + 127);
+                }
             }
         }
         if (p.y8) {
@@ -186,7 +252,7 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_kernel(NormArgs p)
             else
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             const int i = wr * kWave + lane;  // the row's scale bytes in whole lines
-            if (valid && i < pad / 16)
+            if (H && i < pad / 16)
                 store_stream(reinterpret_cast<u32x4 *>(p.y8 + t * p.y8_bytes + p.H) + i,
                              reinterpret_cast<const u32x4 *>(scales[slot])[i]);
             if (WPR > 1)
@@ -214,54 +280,61 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_backward_kernel(No
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int slot = wave / WPR, wr = wave % WPR;
-    const int32_t C = p.H / 8, c0 = GIVEN ? blockIdx.y * (WPR * CH * kWave) : 0;
+    const int32_t c0 = GIVEN ? blockIdx.y * (WPR * CH * 512) : 0;
     float acc[CH][8];
-    Raw8<WFP32> w[CH];
+    Raw8<WFP32, FP32> w[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             acc[i][e] = 0.f;
-        const int32_t c = c0 + (i * WPR + wr) * kWave + lane;
-        if (c < C)
-            w[i].load_cached(p.weight, c);
+        const Columns<FP32> c(c0 + (i * WPR + wr) * 512, lane);
+        w[i].clear();
+#pragma unroll
+        for (int k = 0; k < c.kParts; ++k)
+            if (c.in(k, p.H))
+                w[i].load_cached(p.weight, c, k);
     }
     int parity = 0;
     for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += (int64_t)gridDim.x * kRows) {
         const int64_t t = t0 + slot;
-        const bool valid = t < p.T;
-        Raw8<FP32> h[CH], d[CH];
-        Raw8<false> g[CH];
+        const int32_t H = t < p.T ? p.H : 0;  // no columns in a row past the last
+        Raw8<FP32, FP32> h[CH], d[CH];
+        Raw8<false, FP32> g[CH];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int32_t c = c0 + (i * WPR + wr) * kWave + lane;
-            if (valid && c < C) {
-                h[i].load(p.t, t * C + c);
-                g[i].load(p.grad_y, t * C + c);
-                if (p.grad_x && p.grad_total)
-                    d[i].load(p.grad_total, t * C + c);
-            }
+            const Columns<FP32> c(c0 + (i * WPR + wr) * 512, lane);
+            h[i].clear();
+            g[i].clear();
+            d[i].clear();
+#pragma unroll
+            for (int k = 0; k < c.kParts; ++k)
+                if (c.in(k, H)) {
+                    h[i].load(p.t, t * p.H, c, k);
+                    g[i].load(p.grad_y, t * p.H, c, k);
+                    if (p.grad_x && p.grad_total)
+                        d[i].load(p.grad_total, t * p.H, c, k);
+                }
         }
         if (!WFP32)  // kept as it lies in memory: widened ahead of the loop it would take twice the registers
 #pragma unroll
             for (int i = 0; i < CH; ++i)
-                asm volatile("" : "+v"(w[i].q[0]));
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    asm volatile("" : "+v"(w[i].q[u]));
         RowStats s = {0.f, 0.f};
         if (GIVEN) {
-            if (valid)
+            if (H)
                 s = RowStats{p.stats[2 * t], p.stats[2 * t + 1]};
         } else {
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int32_t c = c0 + (i * WPR + wr) * kWave + lane;
-                if (valid && c < C)
+            for (int i = 0; i < CH; ++i)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        s0 = fmaf(h[i].get(e), h[i].get(e), s0);
-                        s1 = fmaf(g[i].get(e) * w[i].get(e), h[i].get(e), s1);
-                    }
-            }
+                for (int e = 0; e < 8; ++e) {
+                    s0 = fmaf(h[i].get(e), h[i].get(e), s0);
+                    s1 = fmaf(g[i].get(e) * w[i].get(e), h[i].get(e), s1);
+                }
             s0 = wave_sum(s0);
             s1 = wave_sum(s1);
             if (WPR > 1) {
@@ -282,11 +355,17 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_backward_kernel(No
             s.r = rsqrtf(s0 / (float)p.H + p.eps);
             s.c = s1 / (float)p.H * s.r * s.r;
         }
+        // their products are made again: kept across the sums they would take twice the registers
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                asm volatile("" : "+v"(g[i].q[u]));
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int32_t c = c0 + (i * WPR + wr) * kWave + lane;
-            if (!valid || c >= C)
-                continue;
+            const Columns<FP32> c(c0 + (i * WPR + wr) * 512, lane);
+            if (!c.in(0, H))
+                continue;  // the second part lies further right
             if (p.grad_x) {
                 float v[8];
 #pragma unroll
@@ -296,9 +375,12 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_backward_kernel(No
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         v[e] += d[i].get(e);
-                Raw8<FP32> o;
+                Raw8<FP32, FP32> o;
                 o.set(v);
-                o.store(p.grad_x, t * C + c);
+#pragma unroll
+                for (int k = 0; k < c.kParts; ++k)
+                    if (c.in(k, H))
+                        o.store(p.grad_x, t * p.H, c, k);
             }
             if (p.partial)
 #pragma unroll
@@ -330,12 +412,14 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_backward_kernel(No
     float *out = p.partial + (int64_t)blockIdx.x * p.H;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int32_t c = c0 + (i * WPR + wr) * kWave + lane;
-        if (c < C) {
-            reinterpret_cast<u32x4 *>(out)[2 * c] = u32x4{__float_as_uint(acc[i][0]), __float_as_uint(acc[i][1]),
-                                                          __float_as_uint(acc[i][2]), __float_as_uint(acc[i][3])};
-            reinterpret_cast<u32x4 *>(out)[2 * c + 1] = u32x4{__float_as_uint(acc[i][4]), __float_as_uint(acc[i][5]),
-                                                              __float_as_uint(acc[i][6]), __float_as_uint(acc[i][7])};
+        const Columns<FP32> c(c0 + (i * WPR + wr) * 512, lane);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int32_t at = FP32 ? c.at(k) : c.at(0) + k * 4;
+            if (at < p.H)
+                *reinterpret_cast<u32x4 *>(out + at) =
+                    u32x4{__float_as_uint(acc[i][k * 4]), __float_as_uint(acc[i][k * 4 + 1]),
+                          __float_as_uint(acc[i][k * 4 + 2]), __float_as_uint(acc[i][k * 4 + 3])};
         }
     }
 }
@@ -346,17 +430,25 @@ template <bool FP32, bool WFP32>
 __global__ __launch_bounds__(kStatThreads) void rms_norm_stats_kernel(NormGradArgs p)
 {
     __shared__ float part[2][kStatThreads / kWave];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int32_t C = p.H / 8;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         float s0 = 0.f, s1 = 0.f;
-        for (int32_t c = threadIdx.x; c < C; c += kStatThreads) {
-            Raw8<FP32> h;
-            Raw8<false> g;
-            Raw8<WFP32> w;
-            h.load(p.t, t * C + c);
-            g.load(p.grad_y, t * C + c);
-            w.load_cached(p.weight, c);
+        for (int32_t first = wave * 512; first < p.H; first += kStatThreads * 8) {
+            const Columns<FP32> c(first, lane);
+            Raw8<FP32, FP32> h;
+            Raw8<false, FP32> g;
+            Raw8<WFP32, FP32> w;
+            h.clear();
+            g.clear();
+            w.clear();
+#pragma unroll
+            for (int k = 0; k < c.kParts; ++k)
+                if (c.in(k, p.H)) {
+                    h.load(p.t, t * p.H, c, k);
+                    g.load(p.grad_y, t * p.H, c, k);
+                    w.load_cached(p.weight, c, k);
+                }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 s0 = fmaf(h.get(e), h.get(e), s0);
@@ -415,7 +507,8 @@ constexpr int32_t kNormWide = 16384;  // wider rows' gradients take their statis
 
 // Blocks of the gradient's kernel: about as many as the GPU holds at once, each
 // with a partial sum of the weight's gradient. Four rows a block up to 2048
-// columns, else one. (4099 x 7168 in float32: 82.6 us with 512, 85.4 with 1024.)
+// columns, else one. (4099 x 7168 in float32: 82.6 us with 512, 85.4 with 1024,
+// when its rows were not yet read as consecutive bytes.)
 int32_t grad_blocks(int64_t T, int32_t H)
 {
     const int64_t n = H <= 2048 ? (T + 3) / 4 : T, most = H <= 4096 ? 1024 : 512;
