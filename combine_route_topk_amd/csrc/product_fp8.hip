@@ -381,7 +381,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_fp8_kernel(Product8Ar
     };
     const uint32_t units = whole + rest * slices;
     uint32_t u = slot;
-    for (; u < (slices == 4 ? whole : units); u += gridDim.x) {
+    for (; u < (slices > 1 ? whole : units); u += gridDim.x) {
         const auto [l, row0, rows, n0] = unit(u);
         if (!rows)
             continue;
@@ -415,10 +415,11 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_fp8_kernel(Product8Ar
         wait_loads<0>();
         slot_end();
     }
-    static_assert(kSomeThreads == kGemmThreads && kSomeRows * 4 == kTile && kSomeCols == kTile);
-    // A round of slices of 64 rows: product_fp8_some.hpp's loads run further
-    // ahead, 1.1 us for each 128 k where the loop above takes 1.65.
-    if (slices == 4 && u < units) {
+    static_assert(kSomeThreads == kGemmThreads && kSomeRows * 2 == kTile && kSomeCols == kTile);
+    // A round of slices: product_fp8_some.hpp's loads run further ahead. With 64
+    // rows it takes 1.1 us for each 128 k where the loop above takes 1.65 (4 experts
+    // of 64 rows, 7168 by 7168: 51 against 91 us).
+    if (slices > 1 && u < units) {
         const auto [l, row0, rows, n0] = unit(u);
         if (rows)
             some_tile<GRAD, GATED, ACT>(p, lds_offset(lds), l, row0, rows, n0);
@@ -452,32 +453,34 @@ hipError_t launch(const Product8Args &p, int32_t act, bool gated, int cus, hipSt
 }
 
 // Which kernel a product runs on. The host knows max_rows, not how the rows lie:
-// it takes hit = min(max_rows, E_l) experts with rows, and a half-full tile for
-// each beside the full ones. On MI355X, in us, few rows / some rows / tiles:
+// it takes hit = min(max_rows, E_l) experts with rows; up to three quarters of a
+// tile's height each they are taken to have one tile, above that a half-full one
+// beside the full ones. On MI355X, in us, few rows / some rows / tiles:
 //   tiles of 64 rows for less than a quarter of the CUs: 1 expert, 7168 by 2 x
-//   2048: 18 / 42 / 90 at 1 row, 27 / 52 / 91 at 128; 8 experts, 2048 by 2 x 768:
-//   18 / 20 / 32 at 64 rows each;
+//   2048: 25 / 48 / 46 at 64 rows, 26 / 48 / 47 at 128; 8 experts, 2048 by 2 x 768:
+//   17 / 19 / 19 at 64 rows each;
 //   for less than all: 4 experts, 7168 by 7168: 38 / 47 / 90 at 4 rows each,
-//   49 / 43 / 93 at 16, 113 / 55 / 91 at 64;
-//   for all: 32 experts, 7168 by 2 x 2048: 166 / 161 / 206 at one row each,
-//   216 / 164 / 189 at 32, 370 / 169 / 193 at 64, 715 / 249 / 220 at 128; 64
-//   experts, 2048 by 2048: 42 / 43 / 62 at one, 169 / 59 / 65 at 64.
-// A round of tiles over the CUs takes about 1.1 us for each 128 k with 64 rows
-// and 1.9 with 256, which decides between these two.
+//   47 / 34 / 36 at 16, 113 / 51 / 51 at 64;
+//   for all: 32 experts, 7168 by 2 x 2048: 165 / 160 / 197 at one row each,
+//   218 / 164 / 195 at 32, 369 / 169 / 200 at 64, 717 / 195 / 220 at 128; 64
+//   experts, 2048 by 2048: 58 / 45 / 62 at 16, 169 / 58 / 67 at 64, 327 / 79 / 76
+//   at 128.
+// A round of tiles over the CUs takes about 0.9 us for each 128 k with 64 rows,
+// 1.5 with 128 and 1.9 with 256, which decides between the last two.
 enum class Kernel { kFew, kSome, kTiles };
 Kernel choose(const Product8Args &p, bool gated, bool grad, int cus)
 {
     const int64_t rows = p.max_rows, hit = rows < p.El ? rows : p.El;
     const int64_t columns = gated && !grad ? kTile / 2 : kTile, across = (p.N + columns - 1) / columns;
     auto tiles = [&](int64_t height) {
-        const int64_t n = rows / height + hit / 2;
-        return (n > hit ? n : hit) * across;
+        return (4 * rows <= 3 * height * hit ? hit : rows / height + (hit + 1) / 2) * across;
     };
     auto rounds = [&](int64_t n) { return (n + cus - 1) / cus; };
     const int64_t t64 = tiles(64);
     if (!grad && (4 * t64 < cus ? rows <= 128 * (int64_t)p.El : t64 < cus && rows <= 8 * (int64_t)p.El))
         return Kernel::kFew;
-    return rounds(t64) * 11 <= rounds(tiles(kTile)) * 19 ? Kernel::kSome : Kernel::kTiles;
+    const int64_t some = t64 <= cus ? 9 : 15 * rounds(tiles(kSomeRows));
+    return some <= 19 * rounds(tiles(kTile)) ? Kernel::kSome : Kernel::kTiles;
 }
 
 }  // namespace

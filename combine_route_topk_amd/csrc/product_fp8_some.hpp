@@ -4,15 +4,15 @@
 // (product_fp8_few.hip), and too few to fill the 256 rows of product_fp8.hip,
 // whose LDS then holds mostly zeros and whose loads in flight are half A's.
 //
-// A block of eight waves takes up to 64 rows of one expert by 256 rows of W
-// (gated: 128 gate rows and the 128 they gate), 128 k at a time: 40 KiB, in
+// A block of eight waves takes up to 64 or 128 rows of one expert by 256 rows of
+// W (gated: 128 gate rows and the 128 they gate), 128 k at a time: 48 KiB, in
 // three stages. Loads go from memory straight to LDS; while a stage is
 // multiplied the next two are in flight, 64 KiB of W for each CU, and one
 // barrier a stage orders both the stage's arrival and its reuse. Waves 0 to 3
-// take the first 32 rows, waves 4 to 7 the others, 64 rows of W each.
-// On MI355X, 32 experts, 7168 by 2 x 2048: 161 us for 256 rows (5.8 TB/s of
-// weights), 164 for 1024, 169 for 2048; few 178, 216 and 370, tiles of 256 rows
-// 187, 189 and 193.
+// take 16 of each 32 rows, waves 4 to 7 the others, 64 rows of W each.
+// On MI355X, 32 experts, 7168 by 2 x 2048: 160 us for 32 rows (5.8 TB/s of
+// weights), 164 for 1024, 169 for 2048, 195 for 4096; few 165, 218, 369 and 717,
+// tiles of 256 rows 197, 195, 200 and 220.
 #pragma once
 
 #include "product_fp8_device.hpp"
@@ -21,17 +21,18 @@ namespace moe {
 namespace {
 
 constexpr int kSomeThreads = 512;
-constexpr int kSomeRows = 64, kSomeCols = 256, kStages = 3;
+constexpr int kSomeRows = 128, kSomeCols = 256, kStages = 3;
 constexpr int kSomeA = kSomeCols * kTileK8;                       // of A in a stage, behind W
 constexpr int kSomeStage = kSomeA + kSomeRows * kTileK8;
 constexpr int kSomeScales = kStages * kSomeStage, kSomeGroup = kSomeRows * 16;  // scales of four K-tiles, two groups
 constexpr int kSomeLds = kSomeScales + 2 * kSomeGroup;
-constexpr int kSomeLoads = 5;                                     // of a wave for a stage
+constexpr int kSomeLoads = 5;                                     // of a wave for a stage, one more past 64 rows
 
 struct SomeOperands {
     u32x4 w[2], x, s;            // descriptors: 128 rows of W each, the rows, their scales
     uint32_t woff, xoff, soff;   // this lane's bytes in a wave's load
     uint32_t second;             // from one load of W's rows to the next, 64 rows on
+    uint32_t xsecond;            // and of x's; zero where the tile has no more than 64
 };
 
 // Starts a stage's loads, of the 128 k at byte k0 of the rows (kNothing: zeros).
@@ -45,6 +46,8 @@ __device__ __forceinline__ void some_load(const SomeOperands &o, uint32_t dst, u
             // the descriptor's end is checked less the scalar offset, which must not pass it
             load_to_lds(dst + (h * 2 + i) * 8192, o.w[h], o.woff, min(k0 + i * o.second, o.w[h][2]));
     load_to_lds(dst + kSomeA, o.x, o.xoff, min(k0, o.x[2]));
+    if (o.xsecond)
+        load_to_lds(dst + kSomeA + 8192, o.x, o.xoff, min(k0 + o.xsecond, o.x[2]));
 }
 
 // One tile: `rows` rows of expert l from row0 by kCols columns from n0. Every
@@ -68,12 +71,12 @@ __device__ void some_tile(const Product8Args &p, uint32_t lds, int32_t l, int32_
     uint32_t fx[2], fw[2];  // this lane's pieces of a fragment: 16 k of the first 64, and of the second
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-        fx[kk] = lds + kSomeA + frag_row(wr * 32, kk, lane);
+        fx[kk] = lds + kSomeA + frag_row(wr * 16, kk, lane);
         // gated: 32 gate rows, then the 32 up rows 128 further
         fw[kk] = lds + frag_row(PAIR ? wc * 32 : wc * 64, kk, lane);
     }
     constexpr int kUp = (PAIR ? 128 : 32) * kTileK8;  // from fragments 0, 1 to 2, 3
-    const uint32_t scale_at = lds + kSomeScales + (uint32_t)((wr * 32 + (lane & 15)) * 16 + (lane >> 4));
+    const uint32_t scale_at = lds + kSomeScales + (uint32_t)((wr * 16 + (lane & 15)) * 16 + (lane >> 4));
     SomeOperands o;
     const uint8_t *Wl = p.W + (l * wide + n0) * p.K;
 #pragma unroll
@@ -87,8 +90,10 @@ __device__ void some_tile(const Product8Args &p, uint32_t lds, int32_t l, int32_
     o.s = descriptor(x + p.K, __builtin_amdgcn_readfirstlane((uint32_t)(rows * p.a_bytes - p.K)));
     o.woff = (uint32_t)load_row * (uint32_t)p.K + piece;
     o.xoff = (uint32_t)load_row * (uint32_t)p.a_bytes + piece;
-    o.soff = (uint32_t)lane * (uint32_t)p.a_bytes;
+    o.soff = (uint32_t)(wave * kWave + lane) * (uint32_t)p.a_bytes;
     o.second = 64u * (uint32_t)p.K;
+    const bool tall = rows > 64;
+    o.xsecond = tall ? 64u * (uint32_t)p.a_bytes : 0u;
     // the weights' scales along K: of this wave's first 32 rows of W and of its last 32
     const float *ws[2];
 #pragma unroll
@@ -96,10 +101,14 @@ __device__ void some_tile(const Product8Args &p, uint32_t lds, int32_t l, int32_
         const int64_t c = PAIR ? j * (int64_t)p.N + min(n0 + wc * 32, p.N - 32) : min(n0 + wc * 64 + j * 32, p.N - 32);
         ws[j] = p.scale + (l * nbw + c / 128) * nk;
     }
-    f32x4 c[4][2];
+    // rows m * 32 + wr * 16 and on of group m, so that few rows too are shared by all waves
+    constexpr int kGroups = kSomeRows / 32;
+    f32x4 c[4][kGroups];
 #pragma unroll
     for (int g = 0; g < 4; ++g)
-        c[g][0] = c[g][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int m = 0; m < kGroups; ++m)
+            c[g][m] = f32x4{0.f, 0.f, 0.f, 0.f};
     const uint32_t mine = lds + wave * 1024;  // where this wave's loads begin
     auto load_stage = [&](int t) {
         if (t == nk - 1) {  // its pieces past K read as zeros, in x and W alike
@@ -109,15 +118,18 @@ __device__ void some_tile(const Product8Args &p, uint32_t lds, int32_t l, int32_
         some_load(o, mine + t % kStages * kSomeStage, t < nk ? (uint32_t)t * kTileK8 : kNothing);
     };
     auto load_scales = [&](int q) {  // of K-tiles 4 q to 4 q + 3
-        if (wave == 0)
-            load_to_lds(lds + kSomeScales + (q & 1) * kSomeGroup, o.s, o.soff, q * 16);
+        if (wave < kSomeRows / kWave)
+            load_to_lds(lds + kSomeScales + (q & 1) * kSomeGroup + wave * (kWave * 16), o.s, o.soff, q * 16);
     };
     load_scales(0);
     load_stage(0);
     load_stage(1);
     for (int t = 0; t < nk; ++t) {
         // this stage has arrived, and every wave has read the one before it to its end
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kSomeLoads) : "memory");
+        if (tall)
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kSomeLoads + 1) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kSomeLoads) : "memory");
         const float w[2] = {load_uniform(ws[0] + t), load_uniform(ws[1] + t)};
         if ((t & 3) == 0 && t + 4 < nk)
             load_scales((t >> 2) + 1);
@@ -126,35 +138,35 @@ __device__ void some_tile(const Product8Args &p, uint32_t lds, int32_t l, int32_
         uint32_t from = scale_at + (t >> 2 & 1) * kSomeGroup + (t & 3) * 4;
         if (t == nk - 1)  // past K zeros meet the last scale that is one, not what lies behind it
             from -= max((lane >> 4) + 1 - last_scales, 0);
-        if (rows > wr * 32) {
-            i32x8 b[2];
-            uint32_t s[2];
+        if (rows <= wr * 16)
+            continue;
+        i32x8 a[4];
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                b[m] = read_frag(fx[0] + (at + m * 2048), fx[1] + (at + m * 2048));
-                s[m] = lds_read<uint8_t>(from + m * 256);
-            }
+        for (int g = 0; g < 4; ++g)
+            a[g] = read_frag(fw[0] + (at + (g >> 1) * kUp + (g & 1) * 2048), fw[1] + (at + (g >> 1) * kUp + (g & 1) * 2048));
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const uint32_t from_g = at + (g >> 1) * kUp + (g & 1) * 2048;
-                const i32x8 a = read_frag(fw[0] + from_g, fw[1] + from_g);
+        for (int m = 0; m < kGroups; ++m) {
+            if (rows <= m * 32 + wr * 16)
+                break;
+            const i32x8 b = read_frag(fx[0] + (at + m * 4096), fx[1] + (at + m * 4096));
+            const uint32_t s = lds_read<uint8_t>(from + m * 512);
+            f32x4 q[4];
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const f32x4 q = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        a, b[m], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, kOne, 0, s[m]);
+            for (int g = 0; g < 4; ++g)
+                q[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[g], b, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, kOne, 0, s);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        c[g][m][e] = fmaf(w[g >> 1], q[e], c[g][m][e]);
-                }
-            }
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    c[g][m][e] = fmaf(w[g >> 1], q[g][e], c[g][m][e]);
         }
     }
     // the last stage's reads are done before the next tile's loads; those still in flight bring zeros
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-        const int32_t i = wr * 32 + m * 16 + (lane & 15);
-        if (wr * 32 + m * 16 >= rows)
+    for (int m = 0; m < kGroups; ++m) {
+        const int32_t i = m * 32 + wr * 16 + (lane & 15);
+        if (rows <= m * 32 + wr * 16)
             continue;
         const bool in = i < rows;
         if (PAIR) {
