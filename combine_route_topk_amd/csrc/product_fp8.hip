@@ -84,12 +84,14 @@ struct Operand8 {
     }
     // Start the two loads of half H of the K-tile at byte k0 of the rows
     // (kBehind for one behind the last: zeros) into LDS at dst + AT and 8 KiB on.
-    // One block of instructions, so that the reading slot has few.
+    // One block of instructions, so that the reading slot has few. The first load
+    // stands behind five wait states, as its scalar registers need (load_to_lds):
+    // 984 us for 16384 x 8192 by 8192, 979 with three.
     template <int H, int AT>
     __device__ __forceinline__ void load(uint32_t dst, uint32_t k0) const
     {
         uint32_t x, y;
-        asm volatile("s_add_u32 %[x], %[f0], %[k0]\n\ts_add_u32 m0, %[dst], %[at0]\n\ts_min_u32 %[x], %[x], %[end]\n\t"
+        asm volatile("s_add_u32 %[x], %[f0], %[k0]\n\ts_add_u32 m0, %[dst], %[at0]\n\ts_min_u32 %[x], %[x], %[end]\n\ts_nop 1\n\t"
                      "buffer_load_dwordx4 %[v], %[r], %[x] offen lds\n\t"
                      "s_add_u32 %[y], %[f1], %[k0]\n\ts_add_u32 m0, %[dst], %[at1]\n\ts_min_u32 %[y], %[y], %[end]\n\t"
                      "buffer_load_dwordx4 %[v], %[r], %[y] offen lds"

@@ -11,10 +11,13 @@ namespace {
 // compiler does not know of it: it would wait for all such loads in flight
 // before every LDS read. The schedule below orders them with barriers and
 // counted waits instead. (M0 cannot be named as overwritten; nothing else in
-// these kernels uses it.)
+// these kernels uses it.) Nor does it look here for hazards: a scalar register
+// that a vector instruction wrote, such as one read back from where it was
+// spilled, may be read by a load five wait states later, which the block holds
+// itself.
 __device__ __forceinline__ void load_to_lds(uint32_t dst, u32x4 r, uint32_t off, uint32_t soff)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(dst), "v"(off), "s"(r), "s"(soff)
                  : "memory");
