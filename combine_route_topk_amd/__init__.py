@@ -783,6 +783,8 @@ def moe_rms_norm_backward(grad_y: torch.Tensor, total: torch.Tensor, weight: tor
     if need_weight and accumulate and grad_weight is None:
         raise ValueError("accumulate needs grad_weight")
     need = moe_rms_norm_backward_workspace_size(T, H)
+    if not need_weight:
+        need = 8 * T if H > 16384 else 0
     with _on(dev, stream):
         if need_x and grad_x is None:
             grad_x = torch.empty_like(total)

@@ -757,7 +757,7 @@ moe_status_t moe_rms_norm_backward_workspace_size(int64_t T, int32_t H, size_t *
     const moe_status_t s = check_norm(T, H, 0.f, 0, 0);
     if (s != MOE_OK)
         return s;
-    *bytes = moe::rms_norm_backward_workspace_bytes(T, H);
+    *bytes = moe::rms_norm_backward_workspace_bytes(T, H, true);
     return MOE_OK;
 }
 
@@ -777,7 +777,7 @@ moe_status_t moe_rms_norm_backward(const uint16_t *grad_y, const void *total, co
     if (!aligned(grad_y, 16) || !aligned(total, 16) || !aligned(weight, 16) ||
         !aligned(grad_total, 16) || !aligned(grad_x, 16) || !aligned(grad_weight, 4))
         return MOE_ERR_INVALID_ARG;
-    const size_t need = moe::rms_norm_backward_workspace_bytes(T, H);
+    const size_t need = moe::rms_norm_backward_workspace_bytes(T, H, grad_weight != nullptr);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
         return MOE_ERR_WORKSPACE;
     const moe::NormGradArgs p = {grad_y, total, weight, grad_total,

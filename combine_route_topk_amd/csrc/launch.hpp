@@ -168,7 +168,7 @@ struct NormGradArgs {
     void *grad_x;            // or NULL
     float *partial, *stats;  // in the workspace
 };
-size_t rms_norm_backward_workspace_bytes(int64_t T, int32_t H);
+size_t rms_norm_backward_workspace_bytes(int64_t T, int32_t H, bool weight);
 hipError_t launch_rms_norm_backward(NormGradArgs p, bool fp32, bool accumulate, float *grad_weight,
                                     void *workspace, hipStream_t stream);
 

@@ -589,10 +589,10 @@ hipError_t launch_rms_norm(const NormArgs &p, bool fp32, hipStream_t stream)
     return fp32 ? norm_by_width<true, false>(p, stream) : norm_by_width<false, false>(p, stream);
 }
 
-// partial sums of the weight's gradient, then the statistics of wide rows
-size_t rms_norm_backward_workspace_bytes(int64_t T, int32_t H)
+// partial sums of the weight's gradient where it is wanted, then the statistics of wide rows
+size_t rms_norm_backward_workspace_bytes(int64_t T, int32_t H, bool weight)
 {
-    return (size_t)grad_blocks(T, H) * H * 4 + (H > kNormWide ? (size_t)T * 8 : 0);
+    return (weight ? (size_t)grad_blocks(T, H) * H * 4 : 0) + (H > kNormWide ? (size_t)T * 8 : 0);
 }
 
 hipError_t launch_rms_norm_backward(NormGradArgs p, bool fp32, bool accumulate, float *grad_weight, void *workspace,
@@ -600,7 +600,7 @@ hipError_t launch_rms_norm_backward(NormGradArgs p, bool fp32, bool accumulate, 
 {
     const int32_t blocks = grad_blocks(p.T, p.H);
     p.partial = grad_weight ? static_cast<float *>(workspace) : nullptr;
-    p.stats = static_cast<float *>(workspace) + (size_t)blocks * p.H;
+    p.stats = static_cast<float *>(workspace) + (grad_weight ? (size_t)blocks * p.H : 0);
     if (p.T > 0) {
         const hipError_t err =
             p.weight_fp32 ? (fp32 ? norm_grad_by_width<true, true>(p, stream) : norm_grad_by_width<false, true>(p, stream))

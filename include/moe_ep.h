@@ -822,6 +822,7 @@ moe_status_t moe_rms_norm(const void *x, const void *residual, const void *weigh
  *   grad_weight [H] float32 out, or NULL (not both NULL).
  *   workspace   moe_rms_norm_backward_workspace_size() bytes, 16-byte aligned,
  *               contents on entry do not matter (NULL when the size is 0).
+ *               Without grad_weight 8 T bytes where H > 16384, else none (NULL).
  *               Calls that overlap in time must not share a workspace.
  * Errors: as moe_rms_norm; MOE_ERR_WORKSPACE.
  */
