@@ -44,17 +44,17 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_kernel(ProductArgs p)
             continue;  // a slice past the last row
         const int32_t row0 = __builtin_amdgcn_readfirstlane((int32_t)at);
         const int32_t rows = __builtin_amdgcn_readfirstlane((int32_t)min((int64_t)most, r.end - at));
-        gemm.A.init(p.a + (int64_t)row0 * p.K, rows, p.K, p.K, gemm.wave, gemm.lane, 128, [](int j) { return j * 8; });
+        gemm.A.init(p.a + (int64_t)row0 * p.K, rows, p.K, gemm.wave, gemm.lane, 128, [](int j) { return j * 8; });
         const uint16_t *Wl = p.W + (int64_t)l * wide * p.K;
         if constexpr (GRAD) {
             gemm.B.init_strided(Wl + n0, p.K, p.N, p.N - n0, gemm.wave, gemm.lane);
         } else if constexpr (GATED) {
             // rows of a half: for each wave's 32 columns, 16 gate then 16 up
             const bool up = (gemm.wave >> 1) & 1;
-            gemm.B.init(Wl + ((up ? (int64_t)p.N : 0) + n0) * p.K, p.N - n0, p.K, p.K, gemm.wave, gemm.lane, 16,
+            gemm.B.init(Wl + ((up ? (int64_t)p.N : 0) + n0) * p.K, p.N - n0, p.K, gemm.wave, gemm.lane, 16,
                         [](int j) { return (j >> 2) * 32 + (j & 1) * 8; });
         } else {
-            gemm.B.init(Wl + (int64_t)n0 * p.K, p.N - n0, p.K, p.K, gemm.wave, gemm.lane, 32,
+            gemm.B.init(Wl + (int64_t)n0 * p.K, p.N - n0, p.K, gemm.wave, gemm.lane, 32,
                         [](int j) { return (j >> 2) * 64 + (j & 3) * 8; });
         }
         Acc acc;

@@ -53,22 +53,21 @@ struct Operand {
     uint32_t off[2][2];   // this lane's byte offset in load i of half h
     uint32_t tail;        // kOutside where this lane's piece lies past K in the last K-tile
 
-    // K-contiguous: `rows` valid rows of K elements from p, ld elements apart.
-    // half_rows: rows between the halves; row_of: first of the eight rows of
-    // load j of a half.
+    // K-contiguous: `rows` valid rows of K elements from p. half_rows: rows
+    // between the halves; row_of: first of the eight rows of load j of a half.
     template <class RowOf>
-    __device__ __forceinline__ void init(const uint16_t *p, int64_t rows, int32_t K, int32_t ld, int wave, int lane,
+    __device__ __forceinline__ void init(const uint16_t *p, int64_t rows, int32_t K, int wave, int lane,
                                          int half_rows, RowOf row_of)
     {
         static_assert(!STRIDED, "");
         base = reinterpret_cast<const uint8_t *>(p);
-        records = (uint32_t)(max(min(rows, (int64_t)kTile), (int64_t)0) * ld * 2);
+        records = (uint32_t)(max(min(rows, (int64_t)kTile), (int64_t)0) * K * 2);
         const int c = (lane & 7) ^ (lane >> 3);  // piece at LDS position lane % 8 of row lane / 8
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                off[h][i] = (uint32_t)(h * half_rows + row_of(i * 8 + wave) + (lane >> 3)) * (uint32_t)ld * 2u + c * 16;
+                off[h][i] = (uint32_t)(h * half_rows + row_of(i * 8 + wave) + (lane >> 3)) * (uint32_t)K * 2u + c * 16;
         tail = (K & (kTileK - 1)) && c * 8 >= (K & (kTileK - 1)) ? kOutside : 0u;
     }
 
