@@ -1,6 +1,7 @@
 // fp8_device.hpp -- float32 results to E4M3 codes with one power-of-two scale
-// per 32 values, the format of the dispatch payload's rows (fp8.hip). The
-// values are rounded once, from float32 to their codes.
+// per 32 values, the format of the dispatch payload's rows (fp8.hip), whose
+// values are rounded once, from float32 to their codes; and the encoder alone,
+// for weights (quantize_weights.hip).
 #pragma once
 
 #include "device.hpp"
@@ -23,8 +24,9 @@ __device__ __forceinline__ int32_t fp8_exponent(float a)
 __device__ __forceinline__ float fp8_multiplier(int32_t e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
 
 // four values * mul -> four codes, rounded to nearest even; NaN and infinities
-// give the NaN code. mul is a power of two, so the products are exact (a
-// product below float32's normal range lies far below E4M3's smallest code).
+// give the NaN code. Where mul is a power of two, as of the rows, the products
+// are exact (a product below float32's normal range lies far below E4M3's
+// smallest code); by a weights' 1 / scale they are rounded to float32 first.
 __device__ __forceinline__ uint32_t fp8_encode4(float a, float b, float c, float d, float mul)
 {
     const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * mul, b * mul, 0, false);

@@ -117,7 +117,8 @@ __global__ __launch_bounds__(norm_threads(WPR)) void rms_norm_kernel(NormArgs p)
     constexpr int kRows = norm_threads(WPR) / kWave / WPR;
     constexpr int kLines = (WPR * CH * 512 + 4095) / 4096;
     // wider rows need the registers: the weight is read when it is used, the
-    // residual by a few chunks (float32, 1024 x 40960: 104 us, 213 with spills)
+    // residual by a few chunks (float32, 1024 x 40960: 104 us, 213 with many
+    // registers spilled; bf16 rows past 32768 columns still spill three)
     constexpr bool kEarly = WPR < 16 || CH <= 2;
     constexpr int kBatch = kEarly ? CH : (FP32 ? 2 : 4);
     __shared__ float part[2][kRows][WPR];
@@ -507,8 +508,10 @@ constexpr int32_t kNormWide = 16384;  // wider rows' gradients take their statis
 
 // Blocks of the gradient's kernel: about as many as the GPU holds at once, each
 // with a partial sum of the weight's gradient. Four rows a block up to 2048
-// columns, else one. (4099 x 7168 in float32: 82.6 us with 512, 85.4 with 1024,
-// when its rows were not yet read as consecutive bytes.)
+// columns, else one. In us, with 3/4 of these numbers / these / 3/2 / twice them:
+// 4099 x 7168 float32 81.1 / 76.3 / 77.2 / 79.6, bf16 47.8 / 48.5 / 51.3 / 52.8;
+// 32768 x 7168 float32 616 / 592 / 590 / 593; 32768 x 2048 bf16 100 / 94 / 95.5 / 97;
+// 8192 x 4096 bf16 55.1 / 57.2 / 56.4 / 58.5; 2000 x 40000 float32 298 / 301 / 308 / 313.
 int32_t grad_blocks(int64_t T, int32_t H)
 {
     const int64_t n = H <= 2048 ? (T + 3) / 4 : T, most = H <= 4096 ? 1024 : 512;

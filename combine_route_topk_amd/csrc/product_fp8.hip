@@ -13,12 +13,20 @@
 // each accumulator for each K-tile, as an FMA on sums that start from zero would,
 // but no registers for such sums (16384 x 8192 by 8192: 0.99 ms, 1.04 so).
 //
+// What that rounds. The ratio of two units is a reciprocal's product (1 ulp and
+// half of one), and each accumulator's product half an ulp: less than 2^-22 of
+// the sum for each K-tile, 2^-16 at K = 8192, where the result's bf16 keeps 2^-9.
+// Against float64 it shows as a mean of 8e-8 of the results' size at K = 8192, 5e-7
+// at 32768 (the short kernels, which multiply by the scale itself: none), beside an
+// rms of 1.5e-5 from the matrix unit's own sums in all three.
+//
 // On MI355X a round of 256 tiles takes 1.83 us for each K-tile (2.3 PFLOP/s),
-// 16384 x 8192 by 8192 0.99 to 1.05 ms (2.1 to 2.2). Power bounds the K loop: the
+// 16384 x 8192 by 8192 0.98 to 1.05 ms (2.1 to 2.25). Power bounds the K loop: the
 // clock falls to 1.9 GHz in it, and operands of zeros run a fifth faster. Short K is
 // bound by the stores as well: 327680 rows of 2048 by 2 x 768 in 30 rounds take
-// 0.88 ms for the K loop and 0.23 for first loads and bf16 results, or 0.41 with
-// results in both types and pre, 1.8 GB. Starting the next tile's loads before
+// 1.13 ms, 0.91 of them the K loop and 0.22 first loads and bf16 results; with results
+// in both types and pre, 1.8 GB, 1.31 to 1.36 ms, 0.40 of them not the K loop
+// (from K = 128, 2048 and 4096). Starting the next tile's loads before
 // the epilogue, letting its stores run on into that tile's K loop, starting the
 // blocks at different times and stores past the caches gained nothing.
 #include "product_fp8_some.hpp"
@@ -419,8 +427,9 @@ __global__ __launch_bounds__(kGemmThreads, 2) void product_fp8_kernel(Product8Ar
     }
     static_assert(kSomeThreads == kGemmThreads && kSomeRows * 2 == kTile && kSomeCols == kTile);
     // A round of slices: product_fp8_some.hpp's loads run further ahead. With 64
-    // rows it takes 1.1 us for each 128 k where the loop above takes 1.65 (4 experts
-    // of 64 rows, 7168 by 7168: 51 against 91 us).
+    // rows it takes 0.9 us for each 128 k where the loop above takes 1.65 (4 experts
+    // of 64 rows, 7168 by 7168, weights partly in the last-level cache: 51 against
+    // 91 us).
     if (slices > 1 && u < units) {
         const auto [l, row0, rows, n0] = unit(u);
         if (rows)
@@ -457,18 +466,24 @@ hipError_t launch(const Product8Args &p, int32_t act, bool gated, int cus, hipSt
 // Which kernel a product runs on. The host knows max_rows, not how the rows lie:
 // it takes hit = min(max_rows, E_l) experts with rows; up to three quarters of a
 // tile's height each they are taken to have one tile, above that a half-full one
-// beside the full ones. On MI355X, in us, few rows / some rows / tiles:
+// beside the full ones. On MI355X, in us, weights from HBM, rows drawn at random,
+// few rows / some rows / tiles (the last as their 64-row slices where they are few):
 //   tiles of 64 rows for less than a quarter of the CUs: 1 expert, 7168 by 2 x
-//   2048: 25 / 48 / 46 at 64 rows, 26 / 48 / 47 at 128; 8 experts, 2048 by 2 x 768:
-//   17 / 19 / 19 at 64 rows each;
-//   for less than all: 4 experts, 7168 by 7168: 38 / 47 / 90 at 4 rows each,
-//   47 / 34 / 36 at 16, 113 / 51 / 51 at 64;
-//   for all: 32 experts, 7168 by 2 x 2048: 165 / 160 / 197 at one row each,
-//   218 / 164 / 195 at 32, 369 / 169 / 200 at 64, 717 / 195 / 220 at 128; 64
-//   experts, 2048 by 2048: 58 / 45 / 62 at 16, 169 / 58 / 67 at 64, 327 / 79 / 76
+//   2048: 26 / 49 / 50 at 64 and at 128 rows; 8 experts, 2048 by 2 x 768: 10 / 13 / 13
+//   at 8 rows each;
+//   for less than all: 4 experts, 7168 by 7168: 43 / 51 / 51 at 4 rows each,
+//   55 / 54 / 54 at 16, 137 / 62 / 65 at 64;
+//   for all: 32 experts, 7168 by 2 x 2048: 163 / 158 / 188 at one row each,
+//   275 / 162 / 195 at 32, 438 / 169 / 215 at 64, 784 / 268 / 236 at 128; 64
+//   experts, 2048 by 2048: 75 / 54 / 64 at 16, 191 / 64 / 73 at 64, 354 / 96 / 80
 //   at 128.
 // A round of tiles over the CUs takes about 0.9 us for each 128 k with 64 rows,
 // 1.5 with 128 and 1.9 with 256, which decides between the last two.
+// Where the estimate errs: rows that lie evenly leave no half-full tiles beside
+// full ones. The 32 experts with 100 rows each would take 192 us on some rows
+// against 220 (and 240 against 223 where their counts differ by a third); with 128
+// each 211 against 228 (268 against 236 at random). And the 8 experts, at 64 rows,
+// are taken for 72 tiles of 64 where there are 48: 18.8 us, 17.5 on few rows.
 enum class Kernel { kFew, kSome, kTiles };
 Kernel choose(const Product8Args &p, bool gated, bool grad, int cus)
 {

@@ -10,9 +10,9 @@
 // multiplied the next two are in flight, 64 KiB of W for each CU, and one
 // barrier a stage orders both the stage's arrival and its reuse. Waves 0 to 3
 // take 16 of each 32 rows, waves 4 to 7 the others, 64 rows of W each.
-// On MI355X, 32 experts, 7168 by 2 x 2048: 160 us for 32 rows (5.8 TB/s of
-// weights), 164 for 1024, 169 for 2048, 195 for 4096; few 165, 218, 369 and 717,
-// tiles of 256 rows 197, 195, 200 and 220.
+// On MI355X, 32 experts, 7168 by 2 x 2048, rows spread evenly: 158 us for 32 rows
+// (6.0 TB/s of weights), 162 for 1024, 167 for 2048, 211 for 4096; few 163, 215, 372
+// and 715, tiles of 256 rows 188, 192, 211 and 237.
 #pragma once
 
 #include "product_fp8_device.hpp"

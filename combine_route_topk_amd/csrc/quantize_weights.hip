@@ -4,6 +4,10 @@
 //   scale = max|W| of the block / 448 (1 for a block of zeros);
 //   code  = E4M3 nearest to W * (1 / scale)
 //
+// The reciprocal and the product are each rounded to float32 first: a quotient
+// within 2^-23 of itself of the middle between two codes may get the other one
+// than a division would give it. The definition is this one, bit for bit.
+//
 // Bound by HBM: W is read once and each form written once. A block of 256
 // threads takes one 128 x 128 block and holds it in registers between the
 // maximum and the codes, eight rows of eight columns per thread: rows as
@@ -118,7 +122,7 @@ __global__ __launch_bounds__(kQThreads) void quantize_weights_kernel(QuantizeArg
 
 hipError_t launch_quantize_weights(QuantizeArgs p, int64_t n, bool fp32, hipStream_t stream)
 {
-    const int64_t each = (int64_t)((p.O + 127) / 128) * ((p.H + 127) / 128);  // at most 2^18
+    const int64_t each = (int64_t)((p.O + 127) / 128) * ((p.H + 127) / 128);  // at most 2^19
     const int64_t most = kMaxRowBlocks / each;
     const bool stream_in = n * p.O * p.H * (fp32 ? 4 : 2) > kCached;
     for (p.first = 0; p.first < n; p.first += most) {
