@@ -522,10 +522,12 @@ template <bool FP32, bool WFP32, int WPR, int CH>
 hipError_t launch_norm(const NormArgs &p, hipStream_t stream)
 {
     constexpr int kRows = norm_threads(WPR) / kWave / WPR;
+    // a launch takes fewer than 2^32 threads; kMaxRowBlocks of 1024 would be as many
+    constexpr int64_t kMost = kMaxRowBlocks * 256 / norm_threads(WPR);
+    static_assert(kMost * norm_threads(WPR) < (int64_t)1 << 32);
     const int64_t blocks = (p.T + kRows - 1) / kRows;
-    hipLaunchKernelGGL((rms_norm_kernel<FP32, WFP32, WPR, CH>),
-                       dim3((unsigned)(blocks < kMaxRowBlocks ? blocks : kMaxRowBlocks)), dim3(norm_threads(WPR)), 0,
-                       stream, p);
+    hipLaunchKernelGGL((rms_norm_kernel<FP32, WFP32, WPR, CH>), dim3((unsigned)(blocks < kMost ? blocks : kMost)),
+                       dim3(norm_threads(WPR)), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -577,6 +579,7 @@ hipError_t norm_grad_by_width(const NormGradArgs &p, hipStream_t stream)
         return launch_norm_grad<FP32, WFP32, 8, 2>(p, blocks, stream);
     if (p.H <= kNormWide)
         return launch_norm_grad<FP32, WFP32, 16, 2>(p, blocks, stream);
+    static_assert(kMaxRowBlocks * kStatThreads < (int64_t)1 << 32);
     hipLaunchKernelGGL((rms_norm_stats_kernel<FP32, WFP32>), dim3((unsigned)(p.T < kMaxRowBlocks ? p.T : kMaxRowBlocks)),
                        dim3(kStatThreads), 0, stream, p);
     const hipError_t err = hipGetLastError();
